@@ -63,6 +63,23 @@ SIGNATURES = {
     "qlora_linear_bwd_ex": (c_int, [c_void_p, c_void_p, c_void_p, c_int64, c_int64, c_int64, c_int, c_int,
                                     c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_float,
                                     c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "qnf4_act8_quantize": (c_int, [c_void_p, c_int64, c_int64, c_void_p, c_void_p, c_void_p]),
+    "qnf4_act8_dequant": (c_int, [c_void_p, c_void_p, c_int64, c_int64, c_void_p, c_void_p]),
+    "qlora_linear_bwd_act8": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_int64, c_int64, c_int, c_int,
+                                      c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_float,
+                                      c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "qlora_rmsnorm_fwd": (c_int, [c_void_p, c_void_p, c_void_p, c_int64, c_int64, c_double, c_void_p, c_void_p,
+                                  c_void_p, c_void_p, c_void_p, c_void_p]),
+    "qlora_rmsnorm_bwd_workspace_bytes": (c_size_t, [c_int64, c_int64]),
+    "qlora_rmsnorm_bwd": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_int64, c_void_p,
+                                  c_void_p, c_void_p, c_size_t, c_void_p]),
+    "qlora_linear_epi_fwd_workspace_bytes": (c_size_t, [c_int64, c_int64, c_int64, c_int]),
+    "qlora_linear_epi_fwd": (c_int, [c_void_p, c_int64, c_int64, c_int64, c_int, c_int, c_void_p, c_void_p, c_void_p,
+                                     c_void_p, c_void_p, c_void_p, c_int, c_float, c_void_p, c_int, c_void_p, c_void_p,
+                                     c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "qlora_epilogue_bwd_workspace_bytes": (c_size_t, [c_int64, c_int64]),
+    "qlora_epilogue_bwd": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_int64, c_int, c_void_p, c_void_p,
+                                   c_void_p, c_size_t, c_void_p]),
     "qnf4_set_timing_events": (c_int, [c_void_p, c_int]),
     "qlora_linear_plan": (c_int, [c_int64, c_int64, c_int64, c_int, ctypes.POINTER(c_int),
                                   ctypes.POINTER(c_int), ctypes.POINTER(c_int), ctypes.POINTER(c_int)]),
@@ -176,6 +193,26 @@ class NF4Tensor:
         if self.double_quant:
             n += self.scale_codes.numel() + 4 * self.mean.numel()
         return n
+
+
+class Act8Tensor:
+    """An 8-bit checkpoint of a bf16 tensor [M][K]: E4M3 codes [M][ld] (ld = K rounded up to 16)
+    and scale bytes [M][ceil(K / 32)], one power of two per row and 32 features."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, shape):
+        self.codes = codes
+        self.scales = scales
+        self.shape = tuple(shape)
+
+    def nbytes(self) -> int:
+        return self.codes.numel() + self.scales.numel()
+
+
+def _require_act8(a: "Act8Tensor", device, what: str) -> None:
+    M, K = a.shape
+    for t, cols, name in ((a.codes, (K + 15) // 16 * 16, "codes"), (a.scales, (K + 31) // 32, "scales")):
+        if t.dtype != torch.uint8 or tuple(t.shape) != (M, cols) or not t.is_contiguous() or t.device != device:
+            raise QNF4Error(f"the {name} of {what} must be a contiguous uint8 tensor [{M}][{cols}] on {device}")
 
 
 def quantize(W: torch.Tensor, codebook: str = "nf4", double_quant: bool = True,
@@ -301,10 +338,12 @@ def qlora_linear_fwd(x: torch.Tensor, q: NF4Tensor, A: torch.Tensor, B: torch.Te
     return y, t
 
 
-def qlora_linear_bwd(dY: torch.Tensor, x: torch.Tensor, t_saved: torch.Tensor, q: NF4Tensor,
+def qlora_linear_bwd(dY: torch.Tensor, x, t_saved: torch.Tensor, q: NF4Tensor,
                      A: torch.Tensor, B: torch.Tensor, s: float, need_dx: bool = True,
                      workspace: Optional[torch.Tensor] = None):
-    """Returns (dX or None, dA, dB)."""
+    """Returns (dX or None, dA, dB).  x is the forward's bf16 input, or an Act8Tensor of it."""
+    if isinstance(x, Act8Tensor):
+        return _linear_bwd_act8(dY, x, t_saved, q, A, B, s, need_dx, workspace)
     _require_cuda(dY, x, t_saved, A, B)
     M, K = x.shape
     N = q.shape[0]
@@ -321,6 +360,84 @@ def qlora_linear_bwd(dY: torch.Tensor, x: torch.Tensor, t_saved: torch.Tensor, q
                                  _ptr(q.scale_codes), _ptr(q.c2), _ptr(q.mean), _ptr(A), _ptr(B), r, float(s),
                                  _ptr(dX), _ptr(dA), _ptr(dB), _ptr(workspace), workspace.numel(), _stream()),
            "qlora_linear_bwd")
+    return dX, dA, dB
+
+
+def _require(t, dtype, shape, device, name: str) -> None:
+    if t.dtype != dtype or tuple(t.shape) != shape or t.device != device or not t.is_contiguous():
+        raise QNF4Error(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {device}, "
+                        f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _require_weight(q: NF4Tensor, device) -> None:
+    """The stored parts of a quantized weight: types, sizes and device, as the kernels index them."""
+    if len(q.shape) != 2:
+        raise QNF4Error("the quantized weight must have two dimensions")
+    nb = (q.numel + 63) // 64
+    parts = [(q.codes, torch.uint8, 32 * nb, "codes")]
+    if q.double_quant:
+        parts += [(q.scale_codes, torch.uint8, nb, "scale_codes"), (q.c2, torch.float32, (nb + 255) // 256, "c2"),
+                  (q.mean, torch.float32, 1, "mean")]
+    else:
+        parts += [(q.c2, torch.float32, nb, "scales")]
+    for t, dtype, count, name in parts:
+        if t is None or t.dtype != dtype or t.numel() < count or t.device != device or not t.is_contiguous():
+            raise QNF4Error(f"the weight's {name} must hold {count} contiguous {dtype} elements on {device}")
+
+
+def _require_gpu(t: torch.Tensor, name: str) -> torch.device:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise QNF4Error(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def _workspace(given: Optional[torch.Tensor], need: int, device) -> torch.Tensor:
+    """The caller's workspace where it is large enough, else a new one."""
+    if given is None or given.numel() * given.element_size() < need:
+        return torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+    if given.device != device or not given.is_contiguous():
+        raise QNF4Error(f"the workspace must be a contiguous tensor on {device}")
+    return given
+
+
+def _launch(device, what: str, fn, *args) -> None:
+    """fn(*args, stream) with `device` current, on that device's current stream."""
+    if device.index == torch.cuda.current_device():
+        rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    if rc != 0:
+        _check(rc, what)
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _linear_bwd_act8(dY, x: Act8Tensor, t_saved, q: NF4Tensor, A, B, s: float, need_dx: bool, workspace):
+    bf16 = torch.bfloat16
+    dev = _require_gpu(dY, "dY")
+    M, K = x.shape
+    _require_weight(q, dev)
+    N, r = q.shape[0], A.shape[0]
+    if q.shape[1] != K:
+        raise QNF4Error("shape mismatch between x and W")
+    _require_act8(x, dev, "x")
+    _require(dY, bf16, (M, N), dev, "dY")
+    _require(t_saved, torch.float32, (M, r), dev, "t_saved")
+    _require(A, bf16, (r, K), dev, "A")
+    _require(B, bf16, (N, r), dev, "B")
+    dX = torch.empty((M, K), dtype=bf16, device=dev) if need_dx else None
+    dA = torch.empty((r, K), dtype=bf16, device=dev)
+    dB = torch.empty((N, r), dtype=bf16, device=dev)
+    L = lib()
+    ws = _workspace(workspace, L.qlora_linear_bwd_workspace_bytes(M, K, N, r), dev)
+    cb, dq = q._format()
+    _launch(dev, "qlora_linear_bwd_act8", L.qlora_linear_bwd_act8, dY.data_ptr(), x.codes.data_ptr(),
+            x.scales.data_ptr(), t_saved.data_ptr(), M, K, N, cb, dq, q.codes.data_ptr(), _addr(q.scale_codes),
+            q.c2.data_ptr(), _addr(q.mean), A.data_ptr(), B.data_ptr(), r, float(s), _addr(dX), dA.data_ptr(),
+            dB.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
     return dX, dA, dB
 
 

@@ -32,6 +32,7 @@
 #pragma once
 
 #include "nf4_device.cuh"
+#include "epilogue.cuh"
 #include "gemm.h"
 
 namespace qnf4 {
@@ -391,7 +392,7 @@ __device__ __forceinline__ bool mma_run(int count, int k16_tail, uint64_t* ready
   return true;
 }
 
-template <int BN, bool GENERIC, bool A_TMEM>
+template <int BN, bool GENERIC, bool A_TMEM, bool POST>
 __global__ void __launch_bounds__(Cfg<BN, A_TMEM>::kThreads, 1) qlora_gemm_kernel(const __grid_constant__ GemmParams p) {
   using C = Cfg<BN, A_TMEM>;
   constexpr int S = C::kStages;
@@ -701,6 +702,42 @@ __global__ void __launch_bounds__(Cfg<BN, A_TMEM>::kThreads, 1) qlora_gemm_kerne
           else tmem_ld_32x32b_x16(taddr0 + (uint32_t)c0, r);
           tmem_ld_wait();
           if constexpr (kChunk == 32) {
+            if constexpr (POST) {
+              // The thread's feature of 8 tokens at a time: bias, activation and residual in fp32,
+              // one rounding.  The residual arrives as the outputs leave (16 bytes of one token
+              // per thread), so the same 8 x 8 transpose brings it into the accumulator's layout.
+              const int fbase = ti.row0 + 32 * q + (lane & ~7);
+              const float bias = (p.post.bias && row_ok) ? __uint_as_float((uint32_t)p.post.bias[row] << 16) : 0.0f;
+              uint16_t* out = reinterpret_cast<uint16_t*>(p.out);
+#pragma unroll
+              for (int b = 0; b < 4; ++b) {
+                const int col = ti.col0 + c_base + c0 + 8 * b + (lane & 7);
+                const bool ok = col < p.cols && fbase < p.rows;
+                const int64_t at = (int64_t)col * p.ld_out + fbase;
+                float f[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(r[8 * b + j]) + bias;
+                if (p.post.z) {
+                  uint4 v = pack8(f);
+                  transpose8x8_bf16(v.x, v.y, v.z, v.w, lane);
+                  if (ok) *reinterpret_cast<uint4*>(p.post.z + at) = v;
+                }
+                act_apply8(f, p.post.act);
+                if (p.post.residual) {
+                  uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                  if (ok) v = *reinterpret_cast<const uint4*>(p.post.residual + at);
+                  transpose8x8_bf16(v.x, v.y, v.z, v.w, lane);
+                  float g[8];
+                  unpack8(v, g);
+#pragma unroll
+                  for (int j = 0; j < 8; ++j) f[j] += g[j];
+                }
+                uint4 v = pack8(f);
+                transpose8x8_bf16(v.x, v.y, v.z, v.w, lane);
+                if (ok) *reinterpret_cast<uint4*>(out + at) = v;
+              }
+              continue;
+            }
             if (p.epi == kEpiBf16T) {
               // bf16 pairs, then an 8 x 8 transpose per group of 8 lanes: lane j of a group
               // ends up with 8 consecutive output features of token j of each 8-token block,
@@ -722,6 +759,32 @@ __global__ void __launch_bounds__(Cfg<BN, A_TMEM>::kThreads, 1) qlora_gemm_kerne
             }
           }
           if (!row_ok) continue;
+          if constexpr (POST) {
+            // 16-token tiles: two groups of 8 tokens, scalar accesses
+            const float bias = p.post.bias ? __uint_as_float((uint32_t)p.post.bias[row] << 16) : 0.0f;
+            uint16_t* out = reinterpret_cast<uint16_t*>(p.out);
+#pragma unroll
+            for (int j0 = 0; j0 < kChunk; j0 += 8) {
+              float f[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(r[j0 + j]) + bias;
+              const int col0 = ti.col0 + c_base + c0 + j0;
+              if (p.post.z) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                  if (col0 + j < p.cols) p.post.z[(int64_t)(col0 + j) * p.ld_out + row] = f32_to_bf16_bits(f[j]);
+              }
+              act_apply8(f, p.post.act);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                if (col0 + j >= p.cols) continue;
+                const int64_t at = (int64_t)(col0 + j) * p.ld_out + row;
+                const float g = p.post.residual ? __uint_as_float((uint32_t)p.post.residual[at] << 16) : 0.0f;
+                out[at] = f32_to_bf16_bits(f[j] + g);
+              }
+            }
+            continue;
+          }
           if (p.epi == kEpiBf16T) {
             uint16_t* out = reinterpret_cast<uint16_t*>(p.out);
 #pragma unroll
@@ -753,18 +816,26 @@ __global__ void __launch_bounds__(Cfg<BN, A_TMEM>::kThreads, 1) qlora_gemm_kerne
   }
 }
 
-template <int BN, bool GENERIC, bool A_TMEM = false>
-static cudaError_t launch_bn(const GemmParams& p, cudaStream_t st) {
+template <int BN, bool GENERIC, bool A_TMEM, bool POST>
+static cudaError_t launch_bn_post(const GemmParams& p, cudaStream_t st) {
   using C = Cfg<BN, A_TMEM>;
   static std::atomic<uint64_t> configured{0};
-  cudaError_t e = enable_smem_once(qlora_gemm_kernel<BN, GENERIC, A_TMEM>, C::kSmemBytes, configured);
+  cudaError_t e = enable_smem_once(qlora_gemm_kernel<BN, GENERIC, A_TMEM, POST>, C::kSmemBytes, configured);
   if (e != cudaSuccess) return e;
   int dev = 0, sms = 148;
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   const int64_t ntiles = (int64_t)((p.rows + kBM - 1) / kBM) * ((p.cols + BN - 1) / BN) * p.splits;
   const int grid = (int)(ntiles < sms ? ntiles : sms);
-  qlora_gemm_kernel<BN, GENERIC, A_TMEM><<<grid, C::kThreads, C::kSmemBytes, st>>>(p);
+  qlora_gemm_kernel<BN, GENERIC, A_TMEM, POST><<<grid, C::kThreads, C::kSmemBytes, st>>>(p);
   return cudaGetLastError();
+}
+
+// Launches with `post` go to kernels of their own: the plain epilogue keeps its registers.
+template <int BN, bool GENERIC, bool A_TMEM = false>
+static cudaError_t launch_bn(const GemmParams& p, cudaStream_t st) {
+  if (p.has_post)
+    return p.epi == kEpiBf16T ? launch_bn_post<BN, GENERIC, A_TMEM, true>(p, st) : cudaErrorInvalidValue;
+  return launch_bn_post<BN, GENERIC, A_TMEM, false>(p, st);
 }
 
 template <bool GENERIC>
@@ -779,7 +850,8 @@ static cudaError_t launch_gemm_g(const GemmParams& p, int bn, cudaStream_t st) {
     case 32: return launch_bn<32, GENERIC>(p, st);
     case 64: return launch_bn<64, GENERIC>(p, st);
     case 128: return launch_bn<128, GENERIC>(p, st);
-    case 256: return launch_bn<256, GENERIC>(p, st);
+    case 256:   // dX only: the forward's 256-token tiles keep A in tensor memory
+      return p.has_post ? cudaErrorInvalidValue : launch_bn_post<256, GENERIC, false, false>(p, st);
     default: return cudaErrorInvalidValue;
   }
 }

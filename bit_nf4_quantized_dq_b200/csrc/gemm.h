@@ -22,6 +22,15 @@ enum Epi : int32_t {
   kEpiF32T = 1,     // ws[split * split_stride + col * ld + row] = D[row][col]
 };
 
+// What the bf16 epilogue applies behind the product (all parts optional):
+//   z = D + bias,  y = bf16(act(z) + residual).
+struct EpiArgs {
+  const uint16_t* bias;      // bf16 [rows of D] or NULL
+  const uint16_t* residual;  // bf16 [cols of D][rows of D] or NULL
+  uint16_t* z;               // bf16 [cols of D][rows of D] receiving z, or NULL
+  int32_t act;               // Act (epilogue.cuh)
+};
+
 struct GemmSeg {
   int32_t kblocks;    // 64-wide k-blocks in this stretch
   int32_t k16_last;   // 16-wide MMA steps in its last k-block (1..4)
@@ -66,6 +75,8 @@ struct GemmParams {
   void* out;
   int64_t ld_out;
   int64_t split_stride;
+  int32_t has_post;          // kEpiBf16T only: apply `post` before the rounding to bf16
+  EpiArgs post;
 };
 
 // Launch with tile width bn in {16, 32, 64, 128, 256}; grid = (ceil(rows/128), ceil(cols/bn), splits).

@@ -25,34 +25,46 @@
 // error at the level of one fp32 rounding per 64-wide block.
 #pragma once
 
+#include "act8.cuh"
 #include "nf4_device.cuh"
 
 namespace qnf4 {
 
 struct LowRankParams {
-  CUtensorMap a_map;      // A operand (K-major: rows x k, or MN-major: k x rows)
+  CUtensorMap a_map;      // A operand (K-major: rows x k, or MN-major: k x rows; its codes with a8_scales)
   CUtensorMap b_map[3];   // B operand terms, each K-major [cols][k]
   int32_t a_mn;           // A operand is MN-major (two 64-row boxes per k-block)
   int32_t kblocks, k16_last;
   int32_t splits, kb_per_split;
   int32_t rows, cols;     // valid extent: rows on the UMMA M side, cols = rank columns
   double* partial;        // [splits][cols][rows] float64
+  // A operand held as an 8-bit checkpoint (act8.cuh), MN-major: its scales [a8_tokens][a8_groups]
+  const uint8_t* a8_scales;
+  int32_t a8_tokens, a8_groups;
 };
 
 // Warps: 0 and 6 issue TMA loads (alternate k-blocks), 1 issues MMAs, 2-5 and 7-10 flush to
 // float64 (two groups, each draining half of the columns).
 constexpr int kLrThreads = 352;
+// With an 8-bit A operand, warps 11-14 decode it: the codes' box [64 tokens][128 features] lands by
+// TMA, and the bf16 tile that the MMAs read is written beside it in the layout that a TMA load of
+// the bf16 tensor would have left.  Decoding is exact (act8.cuh).
+constexpr int kLrA8Warp0 = 11, kLrA8Warps = 4;
+constexpr int kLrA8Threads = kLrThreads + 32 * kLrA8Warps;
+constexpr int kLrA8CodeBytes = 64 * 128;
 // The accumulator hand-offs between the MMA issuer and the flush warps poll without a
 // suspend hint: each k-block crosses them twice, and a suspended waiter wakes late.
 constexpr bool kLrSpin = true;
 
-template <int BJ, int TERMS>
+template <int BJ, int TERMS, bool A8 = false>
 struct LrCfg {
   static constexpr int BN = BJ * TERMS;            // UMMA N
   static constexpr int kABytes = 128 * 64 * 2;
   static constexpr int kBTermBytes = BJ * 64 * 2;
   static constexpr int kBBytes = TERMS * kBTermBytes;
-  static constexpr int kStageBytes = kABytes + kBBytes;
+  static constexpr int kStageBytes = kABytes + kBBytes + (A8 ? kLrA8CodeBytes : 0);
+  static constexpr int kThreads = A8 ? kLrA8Threads : kLrThreads;
+  static constexpr int kBarrierBytes = A8 ? 512 : 256;
   static constexpr int kStagesRaw = (200 * 1024) / kStageBytes;
   static constexpr int kStages = (kStagesRaw > 8 ? 8 : kStagesRaw) & ~1;   // even: two TMA warps own alternate stages
   // Accumulator buffers in TMEM: the MMA of k-block it writes buffer it % kBufs while the
@@ -60,7 +72,7 @@ struct LrCfg {
   static constexpr int kBufs = (4 * BN <= 512) ? 4 : 2;
   static constexpr int kTmemCols = (kBufs * BN <= 32) ? 32 : (kBufs * BN <= 64) ? 64 : (kBufs * BN <= 128) ? 128
                                    : (kBufs * BN <= 256) ? 256 : 512;
-  static constexpr int kSmemBytes = kStages * kStageBytes + 256 + 1024;
+  static constexpr int kSmemBytes = kStages * kStageBytes + kBarrierBytes + 1024;
   static_assert(BN % 16 == 0 && BN <= 256, "UMMA N");
   static_assert(kBTermBytes % 1024 == 0, "term boxes keep the swizzle atom alignment");
 };
@@ -117,9 +129,10 @@ __device__ __forceinline__ void two_sum_acc(uint64_t& hi, uint64_t& lo, uint64_t
   lo = f2_add(lo, e);
 }
 
-template <int BJ, int TERMS>
-__global__ void __launch_bounds__(kLrThreads, 1) lowrank_kernel(const __grid_constant__ LowRankParams p) {
-  using C = LrCfg<BJ, TERMS>;
+template <int BJ, int TERMS, bool A8>
+__global__ void __launch_bounds__(LrCfg<BJ, TERMS, A8>::kThreads, 1)
+    lowrank_kernel(const __grid_constant__ LowRankParams p) {
+  using C = LrCfg<BJ, TERMS, A8>;
   constexpr int S = C::kStages;
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
@@ -130,6 +143,7 @@ __global__ void __launch_bounds__(kLrThreads, 1) lowrank_kernel(const __grid_con
   uint64_t* accempty = accfull + NB;  // [NB]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(accempty + NB);
   volatile uint32_t* abort_word = tmem_slot + 1;
+  uint64_t* prod = accempty + NB + 1;  // [S] with A8: the decoded A tile is in place (behind the two words above)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row0 = blockIdx.x * 128, col0 = blockIdx.y * BJ, split = blockIdx.z;
@@ -142,6 +156,7 @@ __global__ void __launch_bounds__(kLrThreads, 1) lowrank_kernel(const __grid_con
     for (int s = 0; s < S; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
+      if constexpr (A8) mbar_init(&prod[s], kLrA8Warps);
     }
     for (int b = 0; b < NB; ++b) {
       mbar_init(&accfull[b], 1);
@@ -180,18 +195,19 @@ __global__ void __launch_bounds__(kLrThreads, 1) lowrank_kernel(const __grid_con
       uint8_t* A = smem + s * C::kStageBytes;
       uint8_t* B = A + C::kABytes;
       if (lane == 0) {
-        mbar_arrive_expect_tx(&full[s], C::kABytes + C::kBBytes);
+        mbar_arrive_expect_tx(&full[s], (A8 ? kLrA8CodeBytes : C::kABytes) + C::kBBytes);
         last_issue[s] = it;
       }
       __syncwarp();
       const int k = (kb_begin + it) * 64;
-      const int na = p.a_mn ? 2 : 1;
+      const int na = (p.a_mn && !A8) ? 2 : 1;
       const CUtensorMap* map = nullptr;
       uint8_t* dst = nullptr;
       int cx = 0, cy = 0;
       if (lane < na) {
         map = &p.a_map;
-        if (p.a_mn) { dst = A + lane * 8192; cx = row0 + 64 * lane; cy = k; }
+        if (A8) { dst = B + C::kBBytes; cx = row0; cy = k; }
+        else if (p.a_mn) { dst = A + lane * 8192; cx = row0 + 64 * lane; cy = k; }
         else { dst = A; cx = k; cy = row0; }
       } else if (lane < na + TERMS) {
         const int t = lane - na;
@@ -219,7 +235,8 @@ __global__ void __launch_bounds__(kLrThreads, 1) lowrank_kernel(const __grid_con
         const int buf = it % NB;
         const uint32_t bph = (uint32_t)(it / NB) & 1u;
         if (!mbar_wait_thread<false, kLrSpin>(&accempty[buf], bph ^ 1u, abort_word, kErrWaitMma)) break;
-        if (!mbar_wait_thread(&full[s], ph, abort_word, kErrWaitTma)) break;
+        // with an 8-bit A the decoders arrive on prod[s] after they saw full[s]: it vouches for both
+        if (!mbar_wait_thread(A8 ? &prod[s] : &full[s], ph, abort_word, A8 ? kErrWaitProducer : kErrWaitTma)) break;
         tc_fence_after();
         const uint32_t a_addr = smem_u32(smem + s * C::kStageBytes);
         const uint32_t b_addr = a_addr + C::kABytes;
@@ -241,6 +258,52 @@ __global__ void __launch_bounds__(kLrThreads, 1) lowrank_kernel(const __grid_con
       }
     }
     __syncwarp();
+  } else if (A8 && warp >= kLrA8Warp0) {
+    // ------------------------------------------------------------------ 8-bit decode
+    // A unit is 16 features of one token: one 16-byte code load, two 16-byte stores into the
+    // MN-major tile (chunk j of a token's 128-byte row lands at j ^ (token & 7)).  Thread unit i:
+    // token 8 (2 pw + i % 2) + l % 8, piece (l % 8 + l / 8 + 4 (i / 2)) % 8, so that the 8 lanes of a
+    // 16-byte access phase read 8 different bank groups and write 8 different ones.
+    const int pw = warp - kLrA8Warp0, l8 = lane & 7;
+    int tok[4], pc[4];
+    uint32_t byte[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      tok[i] = 8 * (2 * pw + (i & 1)) + l8;
+      pc[i] = (l8 + (lane >> 3) + 4 * (i >> 1)) & 7;
+    }
+    auto fetch = [&](int it) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = (kb_begin + it) * 64 + tok[i], g = (row0 + 16 * pc[i]) >> 5;
+        byte[i] = (t < p.a8_tokens && g < p.a8_groups) ? __ldg(p.a8_scales + (int64_t)t * p.a8_groups + g) : 127u;
+      }
+    };
+    if (n_iters > 0) fetch(0);
+    for (int it = 0; it < n_iters; ++it) {
+      const int s = it % S;
+      const uint32_t ph = (uint32_t)(it / S) & 1u;
+      uint8_t* A = smem + s * C::kStageBytes;
+      const uint8_t* codes = A + C::kABytes + C::kBBytes;
+      uint32_t cur[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) cur[i] = byte[i];
+      if (it + 1 < n_iters) fetch(it + 1);   // one k-block ahead
+      if (!mbar_wait(&full[s], ph, abort_word, kErrWaitTma)) break;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 q = *reinterpret_cast<const uint4*>(codes + tok[i] * 128 + pc[i] * 16);
+        uint32_t o[8];
+        a8_decode16(q, cur[i], o);
+        uint8_t* row = A + (pc[i] >> 2) * 8192 + tok[i] * 128;
+        const int j = 2 * (pc[i] & 3);
+        *reinterpret_cast<uint4*>(row + ((j ^ (tok[i] & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(row + (((j + 1) ^ (tok[i] & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&prod[s]);
+    }
   } else {
     // ------------------------------------------------------------------ flush to float64
     // Group g (warps 2-5, then 7-10) drains columns [g * HALF, (g + 1) * HALF) of each
@@ -302,19 +365,26 @@ __global__ void __launch_bounds__(kLrThreads, 1) lowrank_kernel(const __grid_con
   }
 }
 
-template <int BJ, int TERMS>
+template <int BJ, int TERMS, bool A8 = false>
 static cudaError_t launch_lowrank_t(const LowRankParams& p, cudaStream_t st) {
-  using C = LrCfg<BJ, TERMS>;
+  using C = LrCfg<BJ, TERMS, A8>;
   static std::atomic<uint64_t> configured{0};
-  cudaError_t e = enable_smem_once(lowrank_kernel<BJ, TERMS>, C::kSmemBytes, configured);
+  cudaError_t e = enable_smem_once(lowrank_kernel<BJ, TERMS, A8>, C::kSmemBytes, configured);
   if (e != cudaSuccess) return e;
   dim3 grid((p.rows + 127) / 128, (p.cols + BJ - 1) / BJ, p.splits);
-  lowrank_kernel<BJ, TERMS><<<grid, kLrThreads, C::kSmemBytes, st>>>(p);
+  lowrank_kernel<BJ, TERMS, A8><<<grid, C::kThreads, C::kSmemBytes, st>>>(p);
   return cudaGetLastError();
 }
 
-// bj in {16, 32, 64}, terms in {1, 3}
+// bj in {16, 32, 64}, terms in {1, 3} (3 with an 8-bit A operand)
 static cudaError_t launch_lowrank(const LowRankParams& p, int bj, int terms, cudaStream_t st) {
+  if (p.a8_scales) {
+    if (terms != 3 || !p.a_mn) return cudaErrorInvalidValue;
+    if (bj == 16) return launch_lowrank_t<16, 3, true>(p, st);
+    if (bj == 32) return launch_lowrank_t<32, 3, true>(p, st);
+    if (bj == 64) return launch_lowrank_t<64, 3, true>(p, st);
+    return cudaErrorInvalidValue;
+  }
   if (terms == 1) {
     if (bj == 16) return launch_lowrank_t<16, 1>(p, st);
     if (bj == 32) return launch_lowrank_t<32, 1>(p, st);

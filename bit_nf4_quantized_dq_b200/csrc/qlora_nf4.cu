@@ -11,6 +11,9 @@
 #include "qlora_nf4.h"
 #include "codec.cuh"
 #include "gemm.cuh"
+#include "act8.cuh"
+#include "rmsnorm.cuh"
+#include "epilogue.cuh"
 #include "lowrank.cuh"
 #include "merge.cuh"
 #include "adamw.cuh"
@@ -143,8 +146,10 @@ struct LinearShape {
   int r;
 };
 
-int check_linear_shape(const LinearShape& s) {
-  if (s.M <= 0 || s.K <= 0 || s.N <= 0 || s.r <= 0) return fail(QNF4_ERR_INVALID, "sizes must be positive");
+// `adapter` false: a linear without adapters (r = 0)
+int check_linear_shape(const LinearShape& s, bool adapter = true) {
+  if (s.M <= 0 || s.K <= 0 || s.N <= 0 || (adapter ? s.r <= 0 : s.r != 0))
+    return fail(QNF4_ERR_INVALID, "sizes must be positive");
   if (s.K % 8 || s.N % 8) return fail(QNF4_ERR_UNSUPPORTED, "K and N must be multiples of 8 (K=%lld N=%lld)",
                                       (long long)s.K, (long long)s.N);
   if (s.r % 8 || s.r > 256) return fail(QNF4_ERR_UNSUPPORTED, "r must be a multiple of 8 in [8, 256] (r=%d)", s.r);
@@ -193,7 +198,8 @@ FwdPlan plan_fwd(const LinearShape& s) {
   p.bn = bn_for(s.M);
   const int64_t tiles = ((s.N + 127) / 128) * ((s.M + p.bn - 1) / p.bn);
   p.splits = choose_splits(tiles, kblocks(s.K));
-  p.t = plan_lowrank(s.M, s.r, s.K);
+  if (s.r > 0) p.t = plan_lowrank(s.M, s.r, s.K);
+  else p.t = LowRankPlan{0, 0};
   return p;
 }
 
@@ -250,12 +256,19 @@ size_t bwd_carve(Carver& c, const LinearShape& s, const BwdPlan& p, BwdWs* w) {
 
 // One low-rank product: A operand map (K-major over [rows][k] or MN-major over [k][rows]),
 // `terms` B maps over [r][k] (K-major), fp64 partials into `partial`.
+// With `a8_scales` the A operand is an 8-bit checkpoint's codes (MN-major, [k][rows]).
 int run_lowrank(const void* a_base, bool a_mn, int64_t a_inner, int64_t a_outer, int64_t a_pitch_bytes,
                 const uint16_t* const* b_terms, int terms, int64_t b_inner, int64_t b_pitch_bytes, int r,
-                int64_t rows, int64_t kdim, const LowRankPlan& pl, double* partial, cudaStream_t st) {
+                int64_t rows, int64_t kdim, const LowRankPlan& pl, double* partial, cudaStream_t st,
+                const uint8_t* a8_scales = nullptr) {
   qnf4::LowRankParams lp;
   memset(&lp, 0, sizeof(lp));
-  if (a_mn) {
+  if (a8_scales) {
+    if (int rc = make_map(&lp.a_map, a_base, false, a_inner, a_outer, a_pitch_bytes, 128, 64)) return rc;
+    lp.a8_scales = a8_scales;
+    lp.a8_tokens = (int32_t)a_outer;
+    lp.a8_groups = (int32_t)qnf4::a8_groups(a_inner);
+  } else if (a_mn) {
     if (int rc = make_map(&lp.a_map, a_base, true, a_inner, a_outer, a_pitch_bytes, 64, 64)) return rc;
   } else {
     if (int rc = make_map(&lp.a_map, a_base, true, a_inner, a_outer, a_pitch_bytes, 64, 128)) return rc;
@@ -348,6 +361,21 @@ int check_format(int double_quant, const uint8_t* codes, const uint8_t* scale_co
   if (double_quant != 0 && double_quant != 1) return fail(QNF4_ERR_INVALID, "double_quant must be 0 or 1");
   if (!codes || !scales || (double_quant && (!scale_codes || !mean))) return fail(QNF4_ERR_INVALID, "NULL pointer");
   if (!aligned(codes, 16)) return fail(QNF4_ERR_UNSUPPORTED, "codes need 16 B alignment");
+  return QNF4_OK;
+}
+
+int check_activation(int activation) {
+  if (activation < QNF4_ACT_NONE || activation > QNF4_ACT_GELU_TANH)
+    return fail(QNF4_ERR_INVALID, "unknown activation %d", activation);
+  return QNF4_OK;
+}
+
+// Sizes of a bf16 tensor [rows][cols] handled row by row in units of 8 values.
+int check_rows(int64_t rows, int64_t cols) {
+  if (rows <= 0 || cols <= 0) return fail(QNF4_ERR_INVALID, "sizes must be positive");
+  if (cols % 8) return fail(QNF4_ERR_UNSUPPORTED, "the row length must be a multiple of 8 (%lld)", (long long)cols);
+  if (rows >= (1ll << 31) || cols >= (1ll << 31) || rows * cols >= (1ll << 40))
+    return fail(QNF4_ERR_INVALID, "sizes too large");
   return QNF4_OK;
 }
 
@@ -709,33 +737,22 @@ int qlora_merge_requantize(const uint8_t* codes, const uint8_t* scale_codes, con
                        gsum, st);
 }
 
-size_t qlora_linear_fwd_workspace_bytes(int64_t M, int64_t K, int64_t N, int r) {
-  LinearShape s{M, K, N, r};
-  if (M <= 0 || K <= 0 || N <= 0 || r <= 0) return 0;
-  Carver c{nullptr};
-  FwdWs w;
-  return fwd_carve(c, s, plan_fwd(s), &w);
-}
+}  // extern "C"
 
-int qlora_linear_fwd(const uint16_t* x, int64_t M, int64_t K, int64_t N, const uint8_t* codes,
-                     const uint8_t* scale_codes, const float* c2, const float* mean, const uint16_t* A,
-                     const uint16_t* B, int r, float s, uint16_t* y, float* t_saved, void* workspace,
-                     size_t workspace_bytes, void* stream) {
-  return qlora_linear_fwd_ex(x, M, K, N, QNF4_CODEBOOK_NF4, 1, codes, scale_codes, c2, mean, A, B, r, s, y, t_saved,
-                             workspace, workspace_bytes, stream);
-}
+namespace {
 
-int qlora_linear_fwd_ex(const uint16_t* x, int64_t M, int64_t K, int64_t N, int codebook, int double_quant,
-                        const uint8_t* codes, const uint8_t* scale_codes, const float* c2, const float* mean,
-                        const uint16_t* A, const uint16_t* B, int r, float s, uint16_t* y, float* t_saved,
-                        void* workspace, size_t workspace_bytes, void* stream) {
-  g_last_error.clear();
-  if (!x || !A || !B || !y || !t_saved || !workspace) return fail(QNF4_ERR_INVALID, "NULL pointer");
+// The forward pass.  A and B may be NULL with r = 0 (no adapter), t_saved NULL (t not wanted);
+// `post` is applied behind the product (NULL: y is the product itself).
+int linear_fwd_impl(const uint16_t* x, const LinearShape& sh, int codebook, int double_quant, const uint8_t* codes,
+                    const uint8_t* scale_codes, const float* c2, const float* mean, const uint16_t* A,
+                    const uint16_t* B, float s, uint16_t* y, float* t_saved, const qnf4::EpiArgs* post,
+                    void* workspace, size_t workspace_bytes, cudaStream_t st) {
+  const int64_t M = sh.M, K = sh.K, N = sh.N;
+  const int r = sh.r;
   if (int rc = check_format(double_quant, codes, scale_codes, c2, mean)) return rc;
   qnf4::Codebook cb;
   if (int rc = get_codebook(codebook, &cb)) return rc;
-  LinearShape sh{M, K, N, r};
-  if (int rc = check_linear_shape(sh)) return rc;
+  if (int rc = check_linear_shape(sh, A != nullptr)) return rc;
   if (!aligned(x, 16) || !aligned(A, 16) || !aligned(B, 16) || !aligned(y, 16) || !aligned(codes, 16) ||
       !aligned(t_saved, 16) || !aligned(workspace, 256))
     return fail(QNF4_ERR_UNSUPPORTED, "alignment: operands 16 B, workspace 256 B");
@@ -745,11 +762,10 @@ int qlora_linear_fwd_ex(const uint16_t* x, int64_t M, int64_t K, int64_t N, int 
   const size_t need = fwd_carve(c, sh, plan, &w);
   if (workspace_bytes < need) return fail(QNF4_ERR_WORKSPACE, "workspace needs %zu bytes", need);
   if (int rc = check_arch()) return rc;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
   mark(0, st);
 
   // 1) t = s x A^T: float64-accumulated partials, then t (fp32) and its bf16 hi / lo parts
-  {
+  if (A) {
     const uint16_t* bt[1] = {A};
     if (int rc = run_lowrank(x, false, K, M, K * 2, bt, 1, K, K * 2, r, M, K, plan.t, w.partial, st)) return rc;
     cudaError_t e = qnf4::launch_finalize_tokens(w.partial, plan.t.splits, M, r, (double)s, t_saved, w.thi, w.tlo,
@@ -767,15 +783,21 @@ int qlora_linear_fwd_ex(const uint16_t* x, int64_t M, int64_t K, int64_t N, int 
     }
     const int bbox = b_box_rows(plan.bn);
     if (int rc = make_map(&gp.maps[1], x, true, K, M, K * 2, 64, bbox)) return rc;
-    if (int rc = make_map(&gp.maps[2], B, true, r, N, (uint64_t)r * 2, 64, 128)) return rc;
-    if (int rc = make_map(&gp.maps[3], w.thi, true, r, M, (uint64_t)r * 2, 64, bbox)) return rc;
-    if (int rc = make_map(&gp.maps[4], w.tlo, true, r, M, (uint64_t)r * 2, 64, bbox)) return rc;
+    if (A) {
+      if (int rc = make_map(&gp.maps[2], B, true, r, N, (uint64_t)r * 2, 64, 128)) return rc;
+      if (int rc = make_map(&gp.maps[3], w.thi, true, r, M, (uint64_t)r * 2, 64, bbox)) return rc;
+      if (int rc = make_map(&gp.maps[4], w.tlo, true, r, M, (uint64_t)r * 2, 64, bbox)) return rc;
+    } else {
+      gp.maps[2] = gp.maps[3] = gp.maps[4] = gp.maps[1];   // prefetched, never read
+    }
     gp.b_box_rows = bbox;
     nf4_operand(gp, cb, double_quant, codes, scale_codes, c2, mean, N, K);
-    gp.nseg = 3;
+    gp.nseg = A ? 3 : 1;
     gp.seg[0] = qnf4::GemmSeg{kblocks(K), k16_last(K), qnf4::kANf4K, 0, 1, 0, 0, 0};
-    gp.seg[1] = qnf4::GemmSeg{kblocks(r), k16_last(r), qnf4::kATmaK, 2, 3, 0, 0, 0};
-    gp.seg[2] = qnf4::GemmSeg{kblocks(r), k16_last(r), qnf4::kATmaK, 2, 4, 0, 0, 0};
+    if (A) {
+      gp.seg[1] = qnf4::GemmSeg{kblocks(r), k16_last(r), qnf4::kATmaK, 2, 3, 0, 0, 0};
+      gp.seg[2] = qnf4::GemmSeg{kblocks(r), k16_last(r), qnf4::kATmaK, 2, 4, 0, 0, 0};
+    }
     if (kATmemForward && plan.bn == 256) {
       // 256-token tiles keep the dequantized W tile (and the adapter matrix rows) in tensor
       // memory, which leaves shared memory for 6 stages instead of 4
@@ -798,16 +820,51 @@ int qlora_linear_fwd_ex(const uint16_t* x, int64_t M, int64_t K, int64_t N, int 
       gp.epi = qnf4::kEpiBf16T;
       gp.out = y;
       gp.ld_out = N;
+      if (post) {
+        gp.has_post = 1;
+        gp.post = *post;
+      }
     }
     cudaError_t e = launch_fused(gp, plan.bn, st);
     if (e != cudaSuccess) return cuda_fail(e, "fused forward launch");
     if (plan.splits > 1) {
-      e = qnf4::launch_reduce_splits_bf16(w.part, plan.splits, M * N, M, N, N, y, N, st);
+      e = post ? qnf4::launch_reduce_splits_epilogue(w.part, plan.splits, M * N, M, N, *post, y, st)
+               : qnf4::launch_reduce_splits_bf16(w.part, plan.splits, M * N, M, N, N, y, N, st);
       if (e != cudaSuccess) return cuda_fail(e, "split reduce launch");
     }
   }
   mark(2, st);
   return QNF4_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t qlora_linear_fwd_workspace_bytes(int64_t M, int64_t K, int64_t N, int r) {
+  LinearShape s{M, K, N, r};
+  if (M <= 0 || K <= 0 || N <= 0 || r <= 0) return 0;
+  Carver c{nullptr};
+  FwdWs w;
+  return fwd_carve(c, s, plan_fwd(s), &w);
+}
+
+int qlora_linear_fwd(const uint16_t* x, int64_t M, int64_t K, int64_t N, const uint8_t* codes,
+                     const uint8_t* scale_codes, const float* c2, const float* mean, const uint16_t* A,
+                     const uint16_t* B, int r, float s, uint16_t* y, float* t_saved, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+  return qlora_linear_fwd_ex(x, M, K, N, QNF4_CODEBOOK_NF4, 1, codes, scale_codes, c2, mean, A, B, r, s, y, t_saved,
+                             workspace, workspace_bytes, stream);
+}
+
+int qlora_linear_fwd_ex(const uint16_t* x, int64_t M, int64_t K, int64_t N, int codebook, int double_quant,
+                        const uint8_t* codes, const uint8_t* scale_codes, const float* c2, const float* mean,
+                        const uint16_t* A, const uint16_t* B, int r, float s, uint16_t* y, float* t_saved,
+                        void* workspace, size_t workspace_bytes, void* stream) {
+  g_last_error.clear();
+  if (!x || !A || !B || !y || !t_saved || !workspace) return fail(QNF4_ERR_INVALID, "NULL pointer");
+  return linear_fwd_impl(x, LinearShape{M, K, N, r}, codebook, double_quant, codes, scale_codes, c2, mean, A, B, s, y,
+                         t_saved, nullptr, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
 }
 
 int qlora_linear_plan(int64_t M, int64_t K, int64_t N, int r, int* fwd_launches, int* bwd_launches,
@@ -826,33 +883,22 @@ int qlora_linear_plan(int64_t M, int64_t K, int64_t N, int r, int* fwd_launches,
   return QNF4_OK;
 }
 
-size_t qlora_linear_bwd_workspace_bytes(int64_t M, int64_t K, int64_t N, int r) {
-  LinearShape s{M, K, N, r};
-  if (M <= 0 || K <= 0 || N <= 0 || r <= 0) return 0;
-  Carver c{nullptr};
-  BwdWs w;
-  return bwd_carve(c, s, plan_bwd(s), &w);
-}
+}  // extern "C"
 
-int qlora_linear_bwd(const uint16_t* dY, const uint16_t* x, const float* t_saved, int64_t M, int64_t K, int64_t N,
-                     const uint8_t* codes, const uint8_t* scale_codes, const float* c2, const float* mean,
-                     const uint16_t* A, const uint16_t* B, int r, float s, uint16_t* dX, uint16_t* dA,
-                     uint16_t* dB, void* workspace, size_t workspace_bytes, void* stream) {
-  return qlora_linear_bwd_ex(dY, x, t_saved, M, K, N, QNF4_CODEBOOK_NF4, 1, codes, scale_codes, c2, mean, A, B, r, s,
-                             dX, dA, dB, workspace, workspace_bytes, stream);
-}
+namespace {
 
-int qlora_linear_bwd_ex(const uint16_t* dY, const uint16_t* x, const float* t_saved, int64_t M, int64_t K, int64_t N,
-                        int codebook, int double_quant, const uint8_t* codes, const uint8_t* scale_codes,
-                        const float* c2, const float* mean, const uint16_t* A, const uint16_t* B, int r, float s,
-                        uint16_t* dX, uint16_t* dA, uint16_t* dB, void* workspace, size_t workspace_bytes,
-                        void* stream) {
-  g_last_error.clear();
+// The backward pass.  With `x_scales`, x is an 8-bit checkpoint's codes [M][a8_ld(K)].
+int linear_bwd_impl(const uint16_t* dY, const void* x, const uint8_t* x_scales, const float* t_saved,
+                    const LinearShape& sh, int codebook, int double_quant, const uint8_t* codes,
+                    const uint8_t* scale_codes, const float* c2, const float* mean, const uint16_t* A,
+                    const uint16_t* B, float s, uint16_t* dX, uint16_t* dA, uint16_t* dB, void* workspace,
+                    size_t workspace_bytes, cudaStream_t st) {
+  const int64_t M = sh.M, K = sh.K, N = sh.N;
+  const int r = sh.r;
   if (!dY || !x || !t_saved || !A || !B || !dA || !dB || !workspace) return fail(QNF4_ERR_INVALID, "NULL pointer");
   if (int rc = check_format(double_quant, codes, scale_codes, c2, mean)) return rc;
   qnf4::Codebook cb;
   if (int rc = get_codebook(codebook, &cb)) return rc;
-  LinearShape sh{M, K, N, r};
   if (int rc = check_linear_shape(sh)) return rc;
   if (!aligned(dY, 16) || !aligned(x, 16) || !aligned(A, 16) || !aligned(B, 16) || !aligned(codes, 16) ||
       !aligned(t_saved, 16) || !aligned(dA, 16) || !aligned(dB, 16) || (dX && !aligned(dX, 16)) ||
@@ -864,7 +910,6 @@ int qlora_linear_bwd_ex(const uint16_t* dY, const uint16_t* x, const float* t_sa
   const size_t need = bwd_carve(c, sh, plan, &w);
   if (workspace_bytes < need) return fail(QNF4_ERR_WORKSPACE, "workspace needs %zu bytes", need);
   if (int rc = check_arch()) return rc;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int64_t ldM = ld8(M);
   cudaError_t e;
   mark(0, st);
@@ -929,7 +974,9 @@ int qlora_linear_bwd_ex(const uint16_t* dY, const uint16_t* x, const float* t_sa
   // 4) dA^T = x^T u (u as three terms), reduced over the M tokens
   {
     const uint16_t* bt[3] = {w.uT3, w.uT3 + (size_t)r * ldM, w.uT3 + (size_t)2 * r * ldM};
-    if (int rc = run_lowrank(x, true, K, M, K * 2, bt, 3, M, ldM * 2, r, K, M, plan.a, w.partial, st)) return rc;
+    const int64_t pitch = x_scales ? qnf4::a8_ld(K) : K * 2;
+    if (int rc = run_lowrank(x, true, K, M, pitch, bt, 3, M, ldM * 2, r, K, M, plan.a, w.partial, st, x_scales))
+      return rc;
     e = qnf4::launch_finalize_grad(w.partial, plan.a.splits, r, K, dA, 0, st);
     if (e != cudaSuccess) return cuda_fail(e, "dA finalize launch");
   }
@@ -945,4 +992,177 @@ int qlora_linear_bwd_ex(const uint16_t* dY, const uint16_t* x, const float* t_sa
   return QNF4_OK;
 }
 
+}  // namespace
+
+extern "C" {
+
+size_t qlora_linear_bwd_workspace_bytes(int64_t M, int64_t K, int64_t N, int r) {
+  LinearShape s{M, K, N, r};
+  if (M <= 0 || K <= 0 || N <= 0 || r <= 0) return 0;
+  Carver c{nullptr};
+  BwdWs w;
+  return bwd_carve(c, s, plan_bwd(s), &w);
+}
+
+int qlora_linear_bwd(const uint16_t* dY, const uint16_t* x, const float* t_saved, int64_t M, int64_t K, int64_t N,
+                     const uint8_t* codes, const uint8_t* scale_codes, const float* c2, const float* mean,
+                     const uint16_t* A, const uint16_t* B, int r, float s, uint16_t* dX, uint16_t* dA,
+                     uint16_t* dB, void* workspace, size_t workspace_bytes, void* stream) {
+  return qlora_linear_bwd_ex(dY, x, t_saved, M, K, N, QNF4_CODEBOOK_NF4, 1, codes, scale_codes, c2, mean, A, B, r, s,
+                             dX, dA, dB, workspace, workspace_bytes, stream);
+}
+
+int qlora_linear_bwd_ex(const uint16_t* dY, const uint16_t* x, const float* t_saved, int64_t M, int64_t K, int64_t N,
+                        int codebook, int double_quant, const uint8_t* codes, const uint8_t* scale_codes,
+                        const float* c2, const float* mean, const uint16_t* A, const uint16_t* B, int r, float s,
+                        uint16_t* dX, uint16_t* dA, uint16_t* dB, void* workspace, size_t workspace_bytes,
+                        void* stream) {
+  g_last_error.clear();
+  return linear_bwd_impl(dY, x, nullptr, t_saved, LinearShape{M, K, N, r}, codebook, double_quant, codes, scale_codes,
+                         c2, mean, A, B, s, dX, dA, dB, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+}
+
+int qlora_linear_bwd_act8(const uint16_t* dY, const uint8_t* x_codes, const uint8_t* x_scales, const float* t_saved,
+                          int64_t M, int64_t K, int64_t N, int codebook, int double_quant, const uint8_t* codes,
+                          const uint8_t* scale_codes, const float* scales, const float* mean, const uint16_t* A,
+                          const uint16_t* B, int r, float s, uint16_t* dX, uint16_t* dA, uint16_t* dB, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  g_last_error.clear();
+  if (!x_scales) return fail(QNF4_ERR_INVALID, "NULL pointer");
+  return linear_bwd_impl(dY, x_codes, x_scales, t_saved, LinearShape{M, K, N, r}, codebook, double_quant, codes,
+                         scale_codes, scales, mean, A, B, s, dX, dA, dB, workspace, workspace_bytes,
+                         static_cast<cudaStream_t>(stream));
+}
+
+int qlora_linear_epi_fwd(const uint16_t* x, int64_t M, int64_t K, int64_t N, int codebook, int double_quant,
+                         const uint8_t* codes, const uint8_t* scale_codes, const float* scales, const float* mean,
+                         const uint16_t* A, const uint16_t* B, int r, float s, const uint16_t* bias, int activation,
+                         const uint16_t* residual, uint16_t* y, float* t_saved, uint16_t* z_saved, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  g_last_error.clear();
+  if (!x || !y || !workspace || (!A != !B)) return fail(QNF4_ERR_INVALID, "NULL pointer");
+  if (!A && (r != 0 || t_saved)) return fail(QNF4_ERR_INVALID, "without adapters r must be 0 and t_saved NULL");
+  if (int rc = check_activation(activation)) return rc;
+  if (!aligned(bias, 16) || !aligned(residual, 16) || !aligned(z_saved, 16))
+    return fail(QNF4_ERR_UNSUPPORTED, "alignment: bias, residual and z_saved 16 B");
+  const qnf4::EpiArgs post{bias, residual, z_saved, activation};
+  return linear_fwd_impl(x, LinearShape{M, K, N, r}, codebook, double_quant, codes, scale_codes, scales, mean, A, B, s,
+                         y, t_saved, &post, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+}
+
+size_t qlora_linear_epi_fwd_workspace_bytes(int64_t M, int64_t K, int64_t N, int r) {
+  if (M <= 0 || K <= 0 || N <= 0 || r < 0) return 0;
+  LinearShape s{M, K, N, r};
+  Carver c{nullptr};
+  FwdWs w;
+  return std::max<size_t>(fwd_carve(c, s, plan_fwd(s), &w), 256);
+}
+
+size_t qlora_epilogue_bwd_workspace_bytes(int64_t M, int64_t N) {
+  if (M <= 0 || N <= 0) return 0;
+  return (size_t)qnf4::epi_bwd_parts(M, N) * (size_t)N * 4;
+}
+
+int qlora_epilogue_bwd(const uint16_t* dY, const uint16_t* z, const uint8_t* z_codes, const uint8_t* z_scales,
+                       int64_t M, int64_t N, int activation, uint16_t* dZ, uint16_t* dbias, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  g_last_error.clear();
+  if (int rc = check_activation(activation)) return rc;
+  const bool act = activation != QNF4_ACT_NONE;
+  if (!dY || (!dZ && act) || (!z_codes != !z_scales)) return fail(QNF4_ERR_INVALID, "NULL pointer");
+  if (act ? !z == !z_codes : (z || z_codes || dZ))
+    return fail(QNF4_ERR_INVALID, act ? "give z either as bf16 or as an 8-bit checkpoint"
+                                      : "without an activation dZ is dY: z and dZ must be NULL");
+  if (!act && !dbias) return fail(QNF4_ERR_INVALID, "nothing to compute");
+  if (int rc = check_rows(M, N)) return rc;
+  if (!aligned(dY, 16) || !aligned(z, 16) || !aligned(dZ, 16) || !aligned(z_codes, 16))
+    return fail(QNF4_ERR_UNSUPPORTED, "alignment: dY, z, its codes and dZ 16 B");
+  if (dbias) {
+    if (!workspace) return fail(QNF4_ERR_INVALID, "NULL pointer");
+    if (!aligned(workspace, 256)) return fail(QNF4_ERR_UNSUPPORTED, "workspace needs 256-byte alignment");
+    const size_t need = qlora_epilogue_bwd_workspace_bytes(M, N);
+    if (workspace_bytes < need) return fail(QNF4_ERR_WORKSPACE, "workspace needs %zu bytes", need);
+  }
+  if (int rc = check_arch()) return rc;
+  qnf4::EpiBwdArgs a;
+  memset(&a, 0, sizeof(a));
+  a.dy = dY;
+  a.z = z;
+  a.z_codes = z_codes;
+  a.z_scales = z_scales;
+  a.M = M;
+  a.N = N;
+  a.dz = dZ;
+  a.partial = static_cast<float*>(workspace);
+  cudaError_t e = qnf4::launch_epilogue_bwd(a, activation, dbias, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "epilogue backward launch");
+  return QNF4_OK;
+}
+
+int qnf4_act8_quantize(const uint16_t* x, int64_t M, int64_t K, uint8_t* codes, uint8_t* scales, void* stream) {
+  g_last_error.clear();
+  if (!x || !codes || !scales) return fail(QNF4_ERR_INVALID, "NULL pointer");
+  if (int rc = check_rows(M, K)) return rc;
+  if (!aligned(x, 16) || !aligned(codes, 16)) return fail(QNF4_ERR_UNSUPPORTED, "alignment: x and codes 16 B");
+  if (int rc = check_arch()) return rc;
+  cudaError_t e = qnf4::launch_act8_quantize(x, M, K, codes, scales, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "act8 quantize launch");
+  return QNF4_OK;
+}
+
+int qnf4_act8_dequant(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_t K, uint16_t* x_out,
+                      void* stream) {
+  g_last_error.clear();
+  if (!codes || !scales || !x_out) return fail(QNF4_ERR_INVALID, "NULL pointer");
+  if (int rc = check_rows(M, K)) return rc;
+  if (!aligned(x_out, 16) || !aligned(codes, 16)) return fail(QNF4_ERR_UNSUPPORTED, "alignment: codes and x_out 16 B");
+  if (int rc = check_arch()) return rc;
+  cudaError_t e = qnf4::launch_act8_dequant(codes, scales, M, K, x_out, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "act8 dequant launch");
+  return QNF4_OK;
+}
+
+int qlora_rmsnorm_fwd(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int64_t M, int64_t K,
+                      double eps, uint16_t* y, uint16_t* h, float* rstd, uint8_t* y_codes, uint8_t* y_scales,
+                      void* stream) {
+  g_last_error.clear();
+  if (!x || !weight || !y || !rstd || (!residual != !h) || (!y_codes != !y_scales))
+    return fail(QNF4_ERR_INVALID, "NULL pointer");
+  if (int rc = check_rows(M, K)) return rc;
+  if (!(eps >= 0.0) || !std::isfinite(eps)) return fail(QNF4_ERR_INVALID, "eps must be finite and >= 0");
+  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(y, 16) || !aligned(h, 16) ||
+      !aligned(y_codes, 16))
+    return fail(QNF4_ERR_UNSUPPORTED, "alignment: bf16 operands and codes 16 B");
+  if (int rc = check_arch()) return rc;
+  qnf4::NormFwdArgs a{x, residual, weight, M, K, (float)eps, y, h, rstd, y_codes, y_scales};
+  cudaError_t e = qnf4::launch_rmsnorm_fwd(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "rmsnorm launch");
+  return QNF4_OK;
+}
+
+size_t qlora_rmsnorm_bwd_workspace_bytes(int64_t M, int64_t K) {
+  if (M <= 0 || K <= 0) return 0;
+  return (size_t)qnf4::norm_bwd_blocks(M, true) * (size_t)K * 4;
+}
+
+int qlora_rmsnorm_bwd(const uint16_t* dy, const uint16_t* dh, const uint16_t* h, const uint16_t* weight,
+                      const float* rstd, int64_t M, int64_t K, uint16_t* dx, uint16_t* dweight, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+  g_last_error.clear();
+  if (!dy || !h || !weight || !rstd || !dx) return fail(QNF4_ERR_INVALID, "NULL pointer");
+  if (int rc = check_rows(M, K)) return rc;
+  if (!aligned(dy, 16) || !aligned(dh, 16) || !aligned(h, 16) || !aligned(weight, 16) || !aligned(dx, 16))
+    return fail(QNF4_ERR_UNSUPPORTED, "alignment: bf16 operands 16 B");
+  if (dweight) {
+    if (!workspace) return fail(QNF4_ERR_INVALID, "NULL pointer");
+    if (!aligned(workspace, 256)) return fail(QNF4_ERR_UNSUPPORTED, "workspace needs 256-byte alignment");
+    const size_t need = qlora_rmsnorm_bwd_workspace_bytes(M, K);
+    if (workspace_bytes < need) return fail(QNF4_ERR_WORKSPACE, "workspace needs %zu bytes", need);
+  }
+  if (int rc = check_arch()) return rc;
+  qnf4::NormBwdArgs a{dy, dh, h, weight, rstd, M, K, dx, dweight ? static_cast<float*>(workspace) : nullptr};
+  cudaError_t e = qnf4::launch_rmsnorm_bwd(a, dweight, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "rmsnorm backward launch");
+  return QNF4_OK;
+}
 }  // extern "C"

@@ -285,6 +285,101 @@ int qlora_adamw_step(float* param, const uint16_t* grad, float* m, float* v, uin
                      void* stream);
 
 /* ---------------------------------------------------------------------------------------
+ * 8-bit activation checkpoints: a bf16 tensor x [M][K] held as E4M3 codes with one power-of-two
+ * scale per row (token) and 32 features, for tensors that only the backward pass reads again
+ * (the input of a linear, the pre-activation of its epilogue).  8.25 bits per value.
+ *
+ *   codes  : uint8 [M][ld], ld = K rounded up to 16, 16-byte aligned; the ld - K codes behind a
+ *            row are 0
+ *   scales : uint8 [M][ceil(K / 32)], scale byte b
+ *   value  = E4M3(code) * 2^(b - 127), exact in bf16; every value of a group with b = 255 is NaN
+ *
+ * qnf4_act8_quantize: with amax the largest magnitude of a group, b - 127 is the smallest integer
+ *   e with amax <= 448 * 2^e, clamped to [-117, 120]; code = E4M3 round-to-nearest-even of
+ *   x * 2^-e (at most 240 where e = 120, so that the value stays finite).  A value of at least
+ *   2^-6 * 2^e is off by at most half an E4M3 step (2^-4 of itself), a smaller one by at most
+ *   2^-10 * 2^e.  A group with a NaN or an infinity gets b = 255.
+ * qnf4_act8_dequant: the values, as bf16.
+ * qlora_linear_bwd_act8: qlora_linear_bwd_ex with x given as a checkpoint; dA is formed from the
+ *   checkpoint's values, the codes are decoded on chip.  Workspace as for qlora_linear_bwd.
+ * Requirements: K % 8 == 0; x, x_out and codes 16-byte aligned.
+ * ------------------------------------------------------------------------------------- */
+int qnf4_act8_quantize(const uint16_t* x, int64_t M, int64_t K, uint8_t* codes, uint8_t* scales, void* stream);
+int qnf4_act8_dequant(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_t K, uint16_t* x_out,
+                      void* stream);
+int qlora_linear_bwd_act8(const uint16_t* dY, const uint8_t* x_codes, const uint8_t* x_scales, const float* t_saved,
+                          int64_t M, int64_t K, int64_t N, int codebook, int double_quant, const uint8_t* codes,
+                          const uint8_t* scale_codes, const float* scales, const float* mean, const uint16_t* A,
+                          const uint16_t* B, int r, float s, uint16_t* dX, uint16_t* dA, uint16_t* dB, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------------------
+ * Root-mean-square norm of the hidden states in front of a linear, with the residual's addition
+ * and an 8-bit checkpoint of the output.
+ *
+ *   v = x + residual (fp32; v = x where residual is NULL)      h = bf16(v)
+ *   rstd = 1 / sqrt(mean_k v^2 + eps)                          y = bf16(v * rstd * weight)
+ *   y_codes, y_scales: what qnf4_act8_quantize makes of y
+ *
+ *   x, residual : bf16[M][K]   weight : bf16[K]   y, h : bf16[M][K]   rstd : float[M]
+ * residual and h are both given or both NULL; y_codes and y_scales likewise.
+ *
+ * Backward, from h (x where there was no residual) and rstd, with n = h * rstd and g = dy * weight:
+ *   dx = dh + rstd * (g - n * mean_k(g * n))     bf16[M][K]; the gradient of x and of the residual
+ *   dweight = sum_m dy * n                        bf16[K], or NULL for a frozen weight
+ * dh : bf16[M][K], the gradient that reaches h through the residual stream, or NULL for none.
+ * The workspace is needed with dweight only: qlora_rmsnorm_bwd_workspace_bytes(M, K) bytes,
+ * 256-byte aligned.
+ * Sums are fp32.  Requirements: K % 8 == 0, eps finite and >= 0, bf16 operands and codes 16-byte
+ * aligned.  No output may overlap an input or another output.
+ * ------------------------------------------------------------------------------------- */
+int qlora_rmsnorm_fwd(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int64_t M, int64_t K,
+                      double eps, uint16_t* y, uint16_t* h, float* rstd, uint8_t* y_codes, uint8_t* y_scales,
+                      void* stream);
+size_t qlora_rmsnorm_bwd_workspace_bytes(int64_t M, int64_t K);
+int qlora_rmsnorm_bwd(const uint16_t* dy, const uint16_t* dh, const uint16_t* h, const uint16_t* weight,
+                      const float* rstd, int64_t M, int64_t K, uint16_t* dx, uint16_t* dweight, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------------------
+ * QLoRA linear with bias, activation and residual in its epilogue.
+ *
+ *   z = x W'^T + s (x A^T) B^T + bias        y = bf16(act(z) + residual)
+ *
+ *   bias : bf16[N] or NULL     residual : bf16[M][N] or NULL
+ *   activation : QNF4_ACT_NONE, _RELU, _SILU (z / (1 + e^-z)), _GELU (z Phi(z)) or _GELU_TANH
+ *     (z / (1 + e^-2u), u = sqrt(2 / pi) (z + 0.044715 z^3))
+ *   A and B may both be NULL with r = 0: a base without adapters (qlora_merge_requantize).
+ *   t_saved : float[M][r] or NULL     z_saved : bf16[M][N] receiving z, or NULL; both are what the
+ *     backward pass reads (serving passes NULL)
+ * z, the activation and the sum with the residual are fp32; y is rounded once.  Everything else
+ * is as for qlora_linear_fwd_ex.  No output may overlap an input or another output.  Workspace:
+ * qlora_linear_epi_fwd_workspace_bytes(M, K, N, r) bytes, 256-byte aligned.
+ *
+ * qlora_epilogue_bwd: dZ = dY * act'(z) (bf16[M][N]) and dbias = sum over tokens of dZ before its
+ * rounding (bf16[N], or NULL), for z as saved or as an 8-bit checkpoint of it (z_codes, z_scales;
+ * z is then NULL).  qlora_linear_bwd takes dZ for its dY; the residual's gradient is dY itself.
+ * With QNF4_ACT_NONE dZ is dY: z and dZ are NULL and only dbias is computed.  The workspace is
+ * needed with dbias only: qlora_epilogue_bwd_workspace_bytes(M, N) bytes, 256-byte aligned.
+ * Requirements: N % 8 == 0; dY, z, z_codes and dZ 16-byte aligned.
+ * ------------------------------------------------------------------------------------- */
+#define QNF4_ACT_NONE 0
+#define QNF4_ACT_RELU 1
+#define QNF4_ACT_SILU 2
+#define QNF4_ACT_GELU 3
+#define QNF4_ACT_GELU_TANH 4
+size_t qlora_linear_epi_fwd_workspace_bytes(int64_t M, int64_t K, int64_t N, int r);
+int qlora_linear_epi_fwd(const uint16_t* x, int64_t M, int64_t K, int64_t N, int codebook, int double_quant,
+                         const uint8_t* codes, const uint8_t* scale_codes, const float* scales, const float* mean,
+                         const uint16_t* A, const uint16_t* B, int r, float s, const uint16_t* bias, int activation,
+                         const uint16_t* residual, uint16_t* y, float* t_saved, uint16_t* z_saved, void* workspace,
+                         size_t workspace_bytes, void* stream);
+size_t qlora_epilogue_bwd_workspace_bytes(int64_t M, int64_t N);
+int qlora_epilogue_bwd(const uint16_t* dY, const uint16_t* z, const uint8_t* z_codes, const uint8_t* z_scales,
+                       int64_t M, int64_t N, int activation, uint16_t* dZ, uint16_t* dbias, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------------------
  * Launch plan of one forward / backward call of this shape (host-only, no device work):
  * the number of kernels each call enqueues, and the split factor of the K loop of the
  * fused dequant GEMMs (1 = no split).  Output pointers are HOST pointers and may be NULL.

@@ -22,9 +22,10 @@ Sources, cited by page title and section:
 
 Pin status of every function is listed in the module docstrings of
 ``oracle.nf4``, ``oracle.linear``, ``oracle.variants`` (the FP4-E2M1 and INT4 code books,
-single-level quantization without double quantization, adapter merge + re-quantization) and
-``oracle.adamw`` (the AdamW step of the paged optimizer).  No function is "parity unpinned": each has
+single-level quantization without double quantization, adapter merge + re-quantization),
+``oracle.adamw`` (the AdamW step of the paged optimizer) and ``oracle.block`` (the operators around
+the linear).  No function is "parity unpinned": each has
 at least one check against the pages or the mathematics in ``tests/``.
 """
 
-from . import nf4, linear, variants, adamw  # noqa: F401
+from . import nf4, linear, variants, adamw, block  # noqa: F401
