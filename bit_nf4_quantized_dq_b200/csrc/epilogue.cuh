@@ -213,8 +213,7 @@ static cudaError_t launch_epilogue_bwd(EpiBwdArgs a, int act, uint16_t* dbias, c
   const dim3 grid((unsigned)((a.N + kEbCols - 1) / kEbCols), (unsigned)parts);
   cudaError_t e = a.z_codes ? launch_epilogue_bwd_z<true>(a, act, grid, st) : launch_epilogue_bwd_z<false>(a, act, grid, st);
   if (e != cudaSuccess || !dbias) return e;
-  column_sum_bf16_kernel<<<(unsigned)((a.N + 255) / 256), 256, 0, st>>>(a.partial, (int)parts, a.N, dbias);
-  return cudaGetLastError();
+  return launch_column_sum(a.partial, (int)parts, a.N, dbias, st);
 }
 
 }  // namespace qnf4

@@ -1142,7 +1142,7 @@ int qlora_rmsnorm_fwd(const uint16_t* x, const uint16_t* residual, const uint16_
 
 size_t qlora_rmsnorm_bwd_workspace_bytes(int64_t M, int64_t K) {
   if (M <= 0 || K <= 0) return 0;
-  return (size_t)qnf4::norm_bwd_blocks(M, true) * (size_t)K * 4;
+  return (size_t)qnf4::norm_bwd_blocks(M) * (size_t)K * 4;
 }
 
 int qlora_rmsnorm_bwd(const uint16_t* dy, const uint16_t* dh, const uint16_t* h, const uint16_t* weight,

@@ -27,8 +27,9 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
 }
 
-// Sum over the block (any multiple of 32 threads up to 1024); every thread gets the result.
-// `slots` holds one float per warp; the same order of additions in every launch.
+// Sum over the block (any multiple of 32 threads up to 1024); every thread gets the result, added in
+// the same order in every launch.  `slots` holds one float per warp; a loop alternates between two
+// sets of slots, so that one barrier per sum is enough.
 __device__ __forceinline__ float block_sum(float v, float* slots) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
@@ -39,9 +40,16 @@ __device__ __forceinline__ float block_sum(float v, float* slots) {
   float s = (int)(threadIdx.x & 31) < warps ? slots[threadIdx.x & 31] : 0.0f;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-  __syncthreads();   // `slots` may be written again
   return s;
 }
+
+// 16 bytes global -> shared, asynchronous (past L1), in groups that the issuing thread waits for.
+__device__ __forceinline__ void cp_async16(uint4* dst, const uint4* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 struct NormFwdArgs {
   const uint16_t* x;
@@ -56,8 +64,70 @@ struct NormFwdArgs {
   uint8_t* scales;
 };
 
-// One block per token; the row is read twice (the second time from L1 / L2).
+// One block per token, each thread with up to VPT units of 8 features in registers, so that x and
+// the residual are read once: an HBM stream of 4 to 8 bytes per value and a block-wide sum between
+// its loads and its stores (several resident blocks cover one another's sums).
+template <int VPT, bool RES, bool A8>
 __global__ void __launch_bounds__(512) rmsnorm_fwd_kernel(const NormFwdArgs a) {
+  __shared__ float slots[32];
+  const int64_t m = blockIdx.x;
+  const int n8 = (int)(a.K / 8), T = blockDim.x;
+  const uint4* x = reinterpret_cast<const uint4*>(a.x + m * a.K);
+  uint4 xv[VPT], rv[VPT];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int c = i * T + threadIdx.x;
+    xv[i] = rv[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (c < n8) {
+      xv[i] = __ldcs(x + c);
+      if constexpr (RES) rv[i] = __ldcs(reinterpret_cast<const uint4*>(a.res + m * a.K) + c);
+    }
+  }
+  float f[VPT][8];
+  float ss = 0.0f;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int c = i * T + threadIdx.x;
+    unpack8(xv[i], f[i]);
+    if constexpr (RES) {
+      float q[8];
+      unpack8(rv[i], q);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[i][j] += q[j];
+      if (c < n8) reinterpret_cast<uint4*>(a.h + m * a.K)[c] = pack8(f[i]);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ss = fmaf(f[i][j], f[i][j], ss);
+  }
+  ss = block_sum(ss, slots);
+  const float rstd = 1.0f / sqrtf(ss / (float)a.K + a.eps);
+  if (threadIdx.x == 0) a.rstd[m] = rstd;
+  const int64_t ld = a8_ld(a.K), G = a8_groups(a.K);
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int c = i * T + threadIdx.x;
+    uint4 yv = make_uint4(0u, 0u, 0u, 0u);
+    if (c < n8) {
+      float q[8];
+      unpack8(__ldg(reinterpret_cast<const uint4*>(a.w) + c), q);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) q[j] *= f[i][j] * rstd;
+      yv = pack8(q);
+      reinterpret_cast<uint4*>(a.y + m * a.K)[c] = yv;
+    }
+    if constexpr (A8) {
+      // the block covers whole groups of 32 features: units past K encode zeros
+      uint2 q8;
+      const uint32_t byte = a8_encode8(yv, q8);
+      if (8 * (int64_t)c < ld) *reinterpret_cast<uint2*>(a.codes + m * ld + 8 * (int64_t)c) = q8;
+      if (c < n8 && (c & 3) == 0) a.scales[m * G + (c >> 2)] = (uint8_t)byte;
+    }
+  }
+}
+
+// Rows too long for the registers of one block: the same, with the row read twice (the second time
+// from L2).
+__global__ void __launch_bounds__(512) rmsnorm_fwd_long_kernel(const NormFwdArgs a) {
   __shared__ float slots[32];
   const int64_t m = blockIdx.x;
   const uint4* x = reinterpret_cast<const uint4*>(a.x + m * a.K);
@@ -79,9 +149,7 @@ __global__ void __launch_bounds__(512) rmsnorm_fwd_kernel(const NormFwdArgs a) {
   const float rstd = 1.0f / sqrtf(ss / (float)a.K + a.eps);
   if (threadIdx.x == 0) a.rstd[m] = rstd;
   const int64_t ld = a8_ld(a.K), G = a8_groups(a.K);
-  // with an 8-bit output the loop covers whole groups of 32 features, so that the four lanes of a
-  // group stay together
-  const int64_t end = a.codes ? 4 * G : n8;
+  const int64_t end = a.codes ? 4 * G : n8;   // whole groups: a group's four lanes stay together
   const int64_t span = (end + blockDim.x - 1) / blockDim.x * blockDim.x;
   for (int64_t c = threadIdx.x; c < span; c += blockDim.x) {
     uint4 yv = make_uint4(0u, 0u, 0u, 0u);
@@ -96,8 +164,8 @@ __global__ void __launch_bounds__(512) rmsnorm_fwd_kernel(const NormFwdArgs a) {
       }
       unpack8(reinterpret_cast<const uint4*>(a.w)[c], q);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = f[i] * rstd * q[i];
-      yv = pack8(f);
+      for (int i = 0; i < 8; ++i) q[i] *= f[i] * rstd;
+      yv = pack8(q);
       reinterpret_cast<uint4*>(a.y + m * a.K)[c] = yv;
     }
     if (a.codes) {
@@ -120,9 +188,105 @@ struct NormBwdArgs {
   float* partial;         // [gridDim.x][K] sums of dy * n, or NULL
 };
 
-// Block b takes the tokens b, b + gridDim.x, ...
+// Block b takes the tokens b, b + gridDim.x, ...; a thread owns up to VPT units of 8 features, the
+// same ones for every token, so the weight's gradient accumulates in its registers and leaves as
+// one row of partial sums per block.  The rows of dy, h and dh of the next S - 1 tokens are on their
+// way into shared memory meanwhile: a thread copies and reads only its own units, so the ring
+// needs no barrier, and a token costs one barrier, that of its sum.
+template <int VPT, int S, bool DH, bool DW>
 __global__ void __launch_bounds__(512) rmsnorm_bwd_kernel(const NormBwdArgs a) {
-  __shared__ float slots[32];
+  extern __shared__ uint4 ring[];   // [stage][dy, h (, dh)][VPT][threads]
+  __shared__ float slots[2][32];
+  constexpr int kRows = DH ? 3 : 2;
+  const int n8 = (int)(a.K / 8), T = blockDim.x;
+  const float inv_k = 1.0f / (float)a.K;
+  uint4* mine = ring + threadIdx.x;
+  auto slot = [&](int stage, int row, int i) { return mine + ((stage * kRows + row) * VPT + i) * T; };
+  auto load = [&](int64_t m, int stage) {
+    if (m < a.M) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int c = i * T + threadIdx.x;
+        if (c < n8) {
+          cp_async16(slot(stage, 0, i), reinterpret_cast<const uint4*>(a.dy + m * a.K) + c);
+          cp_async16(slot(stage, 1, i), reinterpret_cast<const uint4*>(a.h + m * a.K) + c);
+          if constexpr (DH) cp_async16(slot(stage, 2, i), reinterpret_cast<const uint4*>(a.dh + m * a.K) + c);
+        }
+      }
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int s = 0; s < S; ++s) load((int64_t)blockIdx.x + (int64_t)s * gridDim.x, s);
+  uint4 wv[VPT];
+  float acc[VPT][8];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int c = i * T + threadIdx.x;
+    wv[i] = c < n8 ? __ldg(reinterpret_cast<const uint4*>(a.w) + c) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[i][j] = 0.0f;
+  }
+  int stage = 0, flip = 0;
+  for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x) {
+    const float rstd = __ldg(a.rstd + m);
+    cp_async_wait<S - 1>();
+    float dot = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      if (i * T + (int)threadIdx.x >= n8) continue;
+      float d[8], h[8], w[8];
+      unpack8(*slot(stage, 0, i), d);
+      unpack8(*slot(stage, 1, i), h);
+      unpack8(wv[i], w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float n = h[j] * rstd;
+        dot = fmaf(d[j] * w[j], n, dot);
+        if constexpr (DW) acc[i][j] = fmaf(d[j], n, acc[i][j]);
+      }
+    }
+    dot = block_sum(dot, slots[flip]) * inv_k;
+    flip ^= 1;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = i * T + threadIdx.x;
+      if (c >= n8) continue;
+      float d[8], h[8], w[8];
+      unpack8(*slot(stage, 0, i), d);
+      unpack8(*slot(stage, 1, i), h);
+      unpack8(wv[i], w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) d[j] = rstd * (d[j] * w[j] - h[j] * rstd * dot);
+      if constexpr (DH) {
+        float e[8];
+        unpack8(*slot(stage, 2, i), e);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) d[j] += e[j];
+      }
+      reinterpret_cast<uint4*>(a.dx + m * a.K)[c] = pack8(d);
+    }
+    load(m + (int64_t)S * gridDim.x, stage);   // every value of this stage has been used
+    if (++stage == S) stage = 0;
+  }
+  if constexpr (DW) {
+    float* part = a.partial + (int64_t)blockIdx.x * a.K;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = i * T + threadIdx.x;
+      if (c < n8) {
+        reinterpret_cast<float4*>(part)[2 * c] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+        reinterpret_cast<float4*>(part)[2 * c + 1] = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
+      }
+    }
+  }
+}
+
+// Rows too long for the registers of one block: dy and h are read twice, the partial sums of the
+// weight's gradient accumulate in memory.
+__global__ void __launch_bounds__(512) rmsnorm_bwd_long_kernel(const NormBwdArgs a) {
+  __shared__ float slots[2][32];
+  int flip = 0;
   const int64_t n8 = a.K / 8;
   const uint4* w = reinterpret_cast<const uint4*>(a.w);
   float* part = a.partial ? a.partial + (int64_t)blockIdx.x * a.K : nullptr;
@@ -146,7 +310,8 @@ __global__ void __launch_bounds__(512) rmsnorm_bwd_kernel(const NormBwdArgs a) {
         if (part) part[8 * c + i] += d[i] * n;
       }
     }
-    dot = block_sum(dot, slots) / (float)a.K;
+    dot = block_sum(dot, slots[flip]) / (float)a.K;
+    flip ^= 1;
     for (int64_t c = threadIdx.x; c < n8; c += blockDim.x) {
       float d[8], hh[8], ww[8], o[8];
       unpack8(dy[c], d);
@@ -165,40 +330,105 @@ __global__ void __launch_bounds__(512) rmsnorm_bwd_kernel(const NormBwdArgs a) {
   }
 }
 
-// out[k] = bf16(sum_p partial[p][k]), added in the order p = 0 .. parts - 1.
+// out[k] = bf16(sum_p partial[p][k]).  A block owns 32 columns; its warps take every eighth part, and
+// their sums are added in the order of the warps, so the order of additions is fixed.
 __global__ void __launch_bounds__(256) column_sum_bf16_kernel(const float* __restrict__ partial, int parts, int64_t n,
                                                               uint16_t* __restrict__ out) {
-  const int64_t k = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (k >= n) return;
+  __shared__ float sums[8][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t k = (int64_t)blockIdx.x * 32 + lane;
   float s = 0.0f;
-  for (int p = 0; p < parts; ++p) s += partial[(int64_t)p * n + k];
-  out[k] = __bfloat16_as_ushort(__float2bfloat16_rn(s));
+  if (k < n) {
+#pragma unroll 8
+    for (int p = warp; p < parts; p += 8) s += partial[(int64_t)p * n + k];
+  }
+  sums[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && k < n) {
+    float t = sums[0][lane];
+#pragma unroll
+    for (int w = 1; w < 8; ++w) t += sums[w][lane];
+    out[k] = __bfloat16_as_ushort(__float2bfloat16_rn(t));
+  }
 }
 
-static int norm_threads(int64_t k) {
-  const int64_t t = (k / 8 + 31) / 32 * 32;
-  return (int)(t > 512 ? 512 : t);
+static cudaError_t launch_column_sum(const float* partial, int parts, int64_t n, uint16_t* out, cudaStream_t st) {
+  column_sum_bf16_kernel<<<(unsigned)((n + 31) / 32), 256, 0, st>>>(partial, parts, n, out);
+  return cudaGetLastError();
 }
 
-// Blocks of the backward pass: every token has one, up to two per SM when the weight's gradient
-// is wanted (each block leaves one row of partial sums).
-static int norm_bwd_blocks(int64_t M, bool dweight) {
-  const int64_t cap = dweight ? 2 * 148 : (1ll << 31) - 1;
-  return (int)(M < cap ? M : cap);
+// Threads for `units` row units of 8 values, `vpt` per thread.
+static int norm_threads(int64_t units, int vpt) { return (int)(((units + vpt - 1) / vpt + 31) / 32 * 32); }
+
+// Blocks of the backward pass: one per token up to kNormBwdBlocks, which is at most four per SM.
+constexpr int kNormBwdBlocks = 2 * 148;
+static int norm_bwd_blocks(int64_t M) { return (int)(M < kNormBwdBlocks ? M : kNormBwdBlocks); }
+
+constexpr int64_t kNormUnits = 4 * 512;       // row units that one forward block's registers hold
+// Row units of which the backward's ring holds three tokens' dy, h and dh (216 KB of the 227 KB a
+// block may have); above, up to kNormUnits, it holds two.
+constexpr int64_t kNormBwdUnits3 = 4 * 384;
+constexpr int kNormRingMax = 3 * 3 * 16 * (int)kNormBwdUnits3;
+static_assert(2 * 3 * 16 * kNormUnits <= kNormRingMax && kNormRingMax <= 227 * 1024 - 1024, "ring size");
+
+template <int VPT>
+static void launch_rmsnorm_fwd_v(const NormFwdArgs& a, int threads, cudaStream_t st) {
+  const unsigned g = (unsigned)a.M;
+  if (a.res) {
+    if (a.codes) rmsnorm_fwd_kernel<VPT, true, true><<<g, threads, 0, st>>>(a);
+    else rmsnorm_fwd_kernel<VPT, true, false><<<g, threads, 0, st>>>(a);
+  } else {
+    if (a.codes) rmsnorm_fwd_kernel<VPT, false, true><<<g, threads, 0, st>>>(a);
+    else rmsnorm_fwd_kernel<VPT, false, false><<<g, threads, 0, st>>>(a);
+  }
 }
 
 static cudaError_t launch_rmsnorm_fwd(const NormFwdArgs& a, cudaStream_t st) {
-  rmsnorm_fwd_kernel<<<(unsigned)a.M, norm_threads(a.K), 0, st>>>(a);
+  const int64_t units = 4 * a8_groups(a.K);
+  if (units > kNormUnits) rmsnorm_fwd_long_kernel<<<(unsigned)a.M, 512, 0, st>>>(a);
+  else if (units > 512) launch_rmsnorm_fwd_v<4>(a, norm_threads(units, 4), st);
+  else if (units > 64) launch_rmsnorm_fwd_v<2>(a, norm_threads(units, 2), st);
+  else launch_rmsnorm_fwd_v<1>(a, norm_threads(units, 1), st);
   return cudaGetLastError();
 }
 
-static cudaError_t launch_rmsnorm_bwd(const NormBwdArgs& a, uint16_t* dweight, cudaStream_t st) {
-  const int blocks = norm_bwd_blocks(a.M, dweight != nullptr);
-  rmsnorm_bwd_kernel<<<blocks, norm_threads(a.K), 0, st>>>(a);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || !dweight) return e;
-  column_sum_bf16_kernel<<<(unsigned)((a.K + 255) / 256), 256, 0, st>>>(a.partial, blocks, a.K, dweight);
+template <int VPT, int S, bool DH, bool DW>
+static cudaError_t launch_rmsnorm_bwd_t(const NormBwdArgs& a, int blocks, int threads, cudaStream_t st) {
+  const int smem = S * (DH ? 3 : 2) * VPT * threads * 16;
+  static std::atomic<uint64_t> configured{0};
+  cudaError_t e = enable_smem_once(rmsnorm_bwd_kernel<VPT, S, DH, DW>, kNormRingMax, configured);
+  if (e != cudaSuccess) return e;
+  rmsnorm_bwd_kernel<VPT, S, DH, DW><<<blocks, threads, smem, st>>>(a);
   return cudaGetLastError();
+}
+
+template <int VPT, int S>
+static cudaError_t launch_rmsnorm_bwd_v(const NormBwdArgs& a, int blocks, int threads, cudaStream_t st) {
+  if (a.partial)
+    return a.dh ? launch_rmsnorm_bwd_t<VPT, S, true, true>(a, blocks, threads, st)
+                : launch_rmsnorm_bwd_t<VPT, S, false, true>(a, blocks, threads, st);
+  return a.dh ? launch_rmsnorm_bwd_t<VPT, S, true, false>(a, blocks, threads, st)
+              : launch_rmsnorm_bwd_t<VPT, S, false, false>(a, blocks, threads, st);
+}
+
+static cudaError_t launch_rmsnorm_bwd(const NormBwdArgs& a, uint16_t* dweight, cudaStream_t st) {
+  const int blocks = norm_bwd_blocks(a.M);
+  const int64_t units = a.K / 8;
+  cudaError_t e;
+  if (units > kNormUnits) {
+    rmsnorm_bwd_long_kernel<<<blocks, 512, 0, st>>>(a);
+    e = cudaGetLastError();
+  } else if (units > kNormBwdUnits3) {
+    e = launch_rmsnorm_bwd_v<4, 2>(a, blocks, norm_threads(units, 4), st);
+  } else if (units > 1024) {
+    e = launch_rmsnorm_bwd_v<4, 3>(a, blocks, norm_threads(units, 4), st);
+  } else if (units > 64) {
+    e = launch_rmsnorm_bwd_v<2, 3>(a, blocks, norm_threads(units, 2), st);
+  } else {
+    e = launch_rmsnorm_bwd_v<1, 3>(a, blocks, norm_threads(units, 1), st);
+  }
+  if (e != cudaSuccess || !dweight) return e;
+  return launch_column_sum(a.partial, blocks, a.K, dweight, st);
 }
 
 }  // namespace qnf4
