@@ -23,6 +23,46 @@
 
 namespace qnf4 {
 
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+  f[0] = bf_lo(v.x); f[1] = bf_hi(v.x); f[2] = bf_lo(v.y); f[3] = bf_hi(v.y);
+  f[4] = bf_lo(v.z); f[5] = bf_hi(v.z); f[6] = bf_lo(v.w); f[7] = bf_hi(v.w);
+}
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+}
+
+// Two fp32 values in one 64-bit register pair, for the paired arithmetic of sm_100.
+__device__ __forceinline__ uint64_t f32_pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float pair_lo(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float pair_hi(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+__device__ __forceinline__ uint64_t f32x2_mul(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t f32x2_add(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t f32x2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ void unpack8_pairs(const uint4& v, uint64_t (&p)[4]) {
+  p[0] = f32_pair(bf_lo(v.x), bf_hi(v.x));
+  p[1] = f32_pair(bf_lo(v.y), bf_hi(v.y));
+  p[2] = f32_pair(bf_lo(v.z), bf_hi(v.z));
+  p[3] = f32_pair(bf_lo(v.w), bf_hi(v.w));
+}
+
 constexpr int kA8Group = 32;
 constexpr uint32_t kA8NanScale = 255u;
 constexpr uint32_t kA8MinScale = 10u;   // byte of e = -117
@@ -62,20 +102,20 @@ __device__ __forceinline__ uint32_t a8_encode8(const uint4& v, uint2& codes) {
   uint32_t byte = a8_scale_byte(amax);
   if (amax >= 0x7F80u) byte = kA8NanScale;
   const float inv = a8_inv_scale(byte == kA8NanScale ? 127u : byte);
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  float f[8];
+  uint64_t f[4];
+  unpack8_pairs(v, f);
+  uint32_t c[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(w[i] << 16) * inv;
-    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u) * inv;
+    f[i] = f32x2_mul(f[i], f32_pair(inv, inv));
+    c[i] = e4m3x2_encode_hw(pair_lo(f[i]), pair_hi(f[i]));
   }
   if (byte == kA8TopScale) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = fminf(fmaxf(f[i], -240.0f), 240.0f);
+    for (int i = 0; i < 4; ++i)
+      c[i] = e4m3x2_encode_hw(fminf(fmaxf(pair_lo(f[i]), -240.0f), 240.0f),
+                              fminf(fmaxf(pair_hi(f[i]), -240.0f), 240.0f));
   }
-  uint32_t c[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) c[i] = e4m3x2_encode_hw(f[2 * i], f[2 * i + 1]);
   codes.x = c[0] | (c[1] << 16);
   codes.y = c[2] | (c[3] << 16);
   return byte;
@@ -119,20 +159,37 @@ __device__ __forceinline__ void a8_decode16(const uint4& q, uint32_t byte, uint3
   }
 }
 
-// Threads (x along the features, 8 each; y along the tokens).  blockDim.x is a multiple of 4, so a
-// group's four lanes sit in one warp and in one row.
+// Threads (x along the features, 8 each; y along the tokens); each takes kA8Rows tokens and loads
+// all of them first, so that enough bytes are in flight.  blockDim.x is a multiple of 4, so a group's
+// four lanes sit in one warp and in one row.
+constexpr int kA8Rows = 4;
+
 __global__ void __launch_bounds__(256) act8_quantize_kernel(const uint16_t* __restrict__ x, int64_t M, int64_t K,
                                                             uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
   const int64_t ld = a8_ld(K), G = a8_groups(K);
-  const int64_t m = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  const int64_t m0 = (int64_t)blockIdx.x * blockDim.y * kA8Rows + threadIdx.y;
+  const int by = (int)blockDim.y;
+  const int rows = (int)min(M - m0, (int64_t)kA8Rows * by);   // row i of this thread exists while i * by < rows
   for (int64_t c0 = (int64_t)blockIdx.y * blockDim.x; c0 < 4 * G; c0 += (int64_t)gridDim.y * blockDim.x) {
     const int64_t k = 8 * (c0 + threadIdx.x);
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (m < M && k < K) v = *reinterpret_cast<const uint4*>(x + m * K + k);
-    uint2 q;
-    const uint32_t byte = a8_encode8(v, q);
-    if (m < M && k < ld) *reinterpret_cast<uint2*>(codes + m * ld + k) = q;
-    if (m < M && k < K && (threadIdx.x & 3) == 0) scales[m * G + (k >> 5)] = (uint8_t)byte;
+    const uint16_t* src = x + m0 * K + k;
+    uint4 v[kA8Rows];
+    const int in = k < K ? rows : 0;
+#pragma unroll
+    for (int i = 0; i < kA8Rows; ++i, src += by * K) {
+      v[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (i * by < in) v[i] = __ldcs(reinterpret_cast<const uint4*>(src));
+    }
+    const int out = k < ld ? rows : 0, mark = (threadIdx.x & 3) == 0 ? in : 0;
+    uint8_t* dst = codes + m0 * ld + k;
+    uint8_t* sdst = scales + m0 * G + (k >> 5);
+#pragma unroll
+    for (int i = 0; i < kA8Rows; ++i, dst += by * ld, sdst += by * G) {
+      uint2 q;
+      const uint32_t byte = a8_encode8(v[i], q);
+      if (i * by < out) *reinterpret_cast<uint2*>(dst) = q;
+      if (i * by < mark) *sdst = (uint8_t)byte;
+    }
   }
 }
 
@@ -140,15 +197,28 @@ __global__ void __launch_bounds__(256) act8_dequant_kernel(const uint8_t* __rest
                                                            const uint8_t* __restrict__ scales, int64_t M, int64_t K,
                                                            uint16_t* __restrict__ out) {
   const int64_t ld = a8_ld(K), G = a8_groups(K);
-  const int64_t m = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-  if (m >= M) return;
+  const int64_t m0 = (int64_t)blockIdx.x * blockDim.y * kA8Rows + threadIdx.y;
   for (int64_t c = (int64_t)blockIdx.y * blockDim.x + threadIdx.x; c < K / 8; c += (int64_t)gridDim.y * blockDim.x) {
-    const uint2 q = *reinterpret_cast<const uint2*>(codes + m * ld + 8 * c);
-    const float s = a8_scale(scales[m * G + (c >> 2)]);
-    const float2 f0 = a8_decode2(q.x, s), f1 = a8_decode2(q.x >> 16, s), f2 = a8_decode2(q.y, s),
-                 f3 = a8_decode2(q.y >> 16, s);
-    *reinterpret_cast<uint4*>(out + m * K + 8 * c) =
-        make_uint4(pack_bf16x2(f0.x, f0.y), pack_bf16x2(f1.x, f1.y), pack_bf16x2(f2.x, f2.y), pack_bf16x2(f3.x, f3.y));
+    uint2 q[kA8Rows];
+    uint32_t byte[kA8Rows];
+#pragma unroll
+    for (int i = 0; i < kA8Rows; ++i) {
+      const int64_t m = m0 + i * blockDim.y;
+      if (m < M) {
+        q[i] = __ldcs(reinterpret_cast<const uint2*>(codes + m * ld + 8 * c));
+        byte[i] = __ldg(scales + m * G + (c >> 2));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kA8Rows; ++i) {
+      const int64_t m = m0 + i * blockDim.y;
+      if (m >= M) break;
+      const float s = a8_scale(byte[i]);
+      const float2 f0 = a8_decode2(q[i].x, s), f1 = a8_decode2(q[i].x >> 16, s), f2 = a8_decode2(q[i].y, s),
+                   f3 = a8_decode2(q[i].y >> 16, s);
+      *reinterpret_cast<uint4*>(out + m * K + 8 * c) =
+          make_uint4(pack_bf16x2(f0.x, f0.y), pack_bf16x2(f1.x, f1.y), pack_bf16x2(f2.x, f2.y), pack_bf16x2(f3.x, f3.y));
+    }
   }
 }
 
@@ -161,7 +231,7 @@ static void a8_launch_shape(int64_t M, int64_t chunks, dim3* grid, dim3* block) 
   *block = dim3((unsigned)bx, (unsigned)by);
   int64_t gy = (chunks + bx - 1) / bx;
   if (gy > 65535) gy = 65535;
-  *grid = dim3((unsigned)((M + by - 1) / by), (unsigned)gy);
+  *grid = dim3((unsigned)((M + kA8Rows * by - 1) / (kA8Rows * by)), (unsigned)gy);
 }
 
 static cudaError_t launch_act8_quantize(const uint16_t* x, int64_t M, int64_t K, uint8_t* codes, uint8_t* scales,

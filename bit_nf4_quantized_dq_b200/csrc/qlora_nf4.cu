@@ -14,6 +14,7 @@
 #include "act8.cuh"
 #include "rmsnorm.cuh"
 #include "epilogue.cuh"
+#include "fewtoken.cuh"
 #include "lowrank.cuh"
 #include "merge.cuh"
 #include "adamw.cuh"
@@ -763,6 +764,21 @@ int linear_fwd_impl(const uint16_t* x, const LinearShape& sh, int codebook, int 
   if (workspace_bytes < need) return fail(QNF4_ERR_WORKSPACE, "workspace needs %zu bytes", need);
   if (int rc = check_arch()) return rc;
   mark(0, st);
+  if (post && M <= qnf4::kFewTokens) {
+    // the workspace of the tile path holds t (M r floats) with room to spare
+    float* t = A ? (t_saved ? t_saved : static_cast<float*>(workspace)) : nullptr;
+    if (A) {
+      cudaError_t e = qnf4::launch_few_token_down(qnf4::FewTokenDownParams{x, A, (int32_t)M, r, K, s, t}, st);
+      if (e != cudaSuccess) return cuda_fail(e, "few-token down-projection launch");
+    }
+    mark(1, st);
+    const qnf4::FewTokenParams fp{x,  (int32_t)M, K, N, codes, scale_codes, c2, mean, double_quant ? 0 : 1,
+                                  cb, t,          B, r, *post, y};
+    cudaError_t e = qnf4::launch_few_token(fp, st);
+    if (e != cudaSuccess) return cuda_fail(e, "few-token launch");
+    mark(2, st);
+    return QNF4_OK;
+  }
 
   // 1) t = s x A^T: float64-accumulated partials, then t (fp32) and its bf16 hi / lo parts
   if (A) {
@@ -1142,7 +1158,7 @@ int qlora_rmsnorm_fwd(const uint16_t* x, const uint16_t* residual, const uint16_
 
 size_t qlora_rmsnorm_bwd_workspace_bytes(int64_t M, int64_t K) {
   if (M <= 0 || K <= 0) return 0;
-  return (size_t)qnf4::norm_bwd_blocks(M) * (size_t)K * 4;
+  return (size_t)qnf4::norm_bwd_blocks(M, K) * (size_t)K * 4;
 }
 
 int qlora_rmsnorm_bwd(const uint16_t* dy, const uint16_t* dh, const uint16_t* h, const uint16_t* weight,

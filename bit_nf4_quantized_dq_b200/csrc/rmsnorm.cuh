@@ -13,19 +13,11 @@
 // All sums are fp32.
 #pragma once
 
+#include <algorithm>
+
 #include "act8.cuh"
 
 namespace qnf4 {
-
-__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
-__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
-  f[0] = bf_lo(v.x); f[1] = bf_hi(v.x); f[2] = bf_lo(v.y); f[3] = bf_hi(v.y);
-  f[4] = bf_lo(v.z); f[5] = bf_hi(v.z); f[6] = bf_lo(v.w); f[7] = bf_hi(v.w);
-}
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
-}
 
 // Sum over the block (any multiple of 32 threads up to 1024); every thread gets the result, added in
 // the same order in every launch.  `slots` holds one float per warp; a loop alternates between two
@@ -193,11 +185,13 @@ struct NormBwdArgs {
 // one row of partial sums per block.  The rows of dy, h and dh of the next S - 1 tokens are on their
 // way into shared memory meanwhile: a thread copies and reads only its own units, so the ring
 // needs no barrier, and a token costs one barrier, that of its sum.
+// (96 registers at VPT = 2: two blocks of 320 threads per SM at K = 5120.)
 template <int VPT, int S, bool DH, bool DW>
-__global__ void __launch_bounds__(512) rmsnorm_bwd_kernel(const NormBwdArgs a) {
+__global__ void __maxnreg__(VPT <= 2 ? 96 : 128) rmsnorm_bwd_kernel(const NormBwdArgs a) {
   extern __shared__ uint4 ring[];   // [stage][dy, h (, dh)][VPT][threads]
   __shared__ float slots[2][32];
   constexpr int kRows = DH ? 3 : 2;
+  constexpr bool kKeep = VPT <= 2;   // g and n stay in registers across the sum, else they are formed again
   const int n8 = (int)(a.K / 8), T = blockDim.x;
   const float inv_k = 1.0f / (float)a.K;
   uint4* mine = ring + threadIdx.x;
@@ -218,53 +212,62 @@ __global__ void __launch_bounds__(512) rmsnorm_bwd_kernel(const NormBwdArgs a) {
   };
 #pragma unroll
   for (int s = 0; s < S; ++s) load((int64_t)blockIdx.x + (int64_t)s * gridDim.x, s);
-  uint4 wv[VPT];
-  float acc[VPT][8];
+  // pairs of fp32 values throughout: the paired instructions halve the arithmetic
+  uint64_t w2[VPT][4], acc[DW ? VPT : 1][4];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int c = i * T + threadIdx.x;
-    wv[i] = c < n8 ? __ldg(reinterpret_cast<const uint4*>(a.w) + c) : make_uint4(0u, 0u, 0u, 0u);
+    unpack8_pairs(c < n8 ? __ldg(reinterpret_cast<const uint4*>(a.w) + c) : make_uint4(0u, 0u, 0u, 0u), w2[i]);
+    if constexpr (DW) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[i][j] = 0.0f;
+      for (int j = 0; j < 4; ++j) acc[i][j] = 0ull;
+    }
   }
   int stage = 0, flip = 0;
   for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x) {
     const float rstd = __ldg(a.rstd + m);
+    const uint64_t r2 = f32_pair(rstd, rstd);
     cp_async_wait<S - 1>();
-    float dot = 0.0f;
+    uint64_t g2[kKeep ? VPT : 1][4], n2[kKeep ? VPT : 1][4], dot2 = 0ull;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       if (i * T + (int)threadIdx.x >= n8) continue;
-      float d[8], h[8], w[8];
-      unpack8(*slot(stage, 0, i), d);
-      unpack8(*slot(stage, 1, i), h);
-      unpack8(wv[i], w);
+      const int k = kKeep ? i : 0;
+      uint64_t d[4];
+      unpack8_pairs(*slot(stage, 0, i), d);
+      unpack8_pairs(*slot(stage, 1, i), n2[k]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float n = h[j] * rstd;
-        dot = fmaf(d[j] * w[j], n, dot);
-        if constexpr (DW) acc[i][j] = fmaf(d[j], n, acc[i][j]);
+      for (int j = 0; j < 4; ++j) {
+        n2[k][j] = f32x2_mul(n2[k][j], r2);
+        g2[k][j] = f32x2_mul(d[j], w2[i][j]);
+        dot2 = f32x2_fma(g2[k][j], n2[k][j], dot2);
+        if constexpr (DW) acc[i][j] = f32x2_fma(d[j], n2[k][j], acc[i][j]);
       }
     }
-    dot = block_sum(dot, slots[flip]) * inv_k;
+    const float dot = block_sum(pair_lo(dot2) + pair_hi(dot2), slots[flip]) * inv_k;
     flip ^= 1;
+    const uint64_t c2 = f32_pair(-rstd * dot, -rstd * dot);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int c = i * T + threadIdx.x;
       if (c >= n8) continue;
-      float d[8], h[8], w[8];
-      unpack8(*slot(stage, 0, i), d);
-      unpack8(*slot(stage, 1, i), h);
-      unpack8(wv[i], w);
+      const int k = kKeep ? i : 0;
+      uint64_t e[4] = {0ull, 0ull, 0ull, 0ull};
+      if constexpr (!kKeep) {
+        unpack8_pairs(*slot(stage, 0, i), g2[0]);
+        unpack8_pairs(*slot(stage, 1, i), n2[0]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) d[j] = rstd * (d[j] * w[j] - h[j] * rstd * dot);
-      if constexpr (DH) {
-        float e[8];
-        unpack8(*slot(stage, 2, i), e);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) d[j] += e[j];
+        for (int j = 0; j < 4; ++j) {
+          n2[0][j] = f32x2_mul(n2[0][j], r2);
+          g2[0][j] = f32x2_mul(g2[0][j], w2[i][j]);
+        }
       }
-      reinterpret_cast<uint4*>(a.dx + m * a.K)[c] = pack8(d);
+      if constexpr (DH) unpack8_pairs(*slot(stage, 2, i), e);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) e[j] = f32x2_fma(n2[k][j], c2, f32x2_fma(g2[k][j], r2, e[j]));
+      reinterpret_cast<uint4*>(a.dx + m * a.K)[c] =
+          make_uint4(pack_bf16x2(pair_lo(e[0]), pair_hi(e[0])), pack_bf16x2(pair_lo(e[1]), pair_hi(e[1])),
+                     pack_bf16x2(pair_lo(e[2]), pair_hi(e[2])), pack_bf16x2(pair_lo(e[3]), pair_hi(e[3])));
     }
     load(m + (int64_t)S * gridDim.x, stage);   // every value of this stage has been used
     if (++stage == S) stage = 0;
@@ -275,8 +278,8 @@ __global__ void __launch_bounds__(512) rmsnorm_bwd_kernel(const NormBwdArgs a) {
     for (int i = 0; i < VPT; ++i) {
       const int c = i * T + threadIdx.x;
       if (c < n8) {
-        reinterpret_cast<float4*>(part)[2 * c] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
-        reinterpret_cast<float4*>(part)[2 * c + 1] = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
+        reinterpret_cast<ulonglong2*>(part)[2 * c] = make_ulonglong2(acc[i][0], acc[i][1]);
+        reinterpret_cast<ulonglong2*>(part)[2 * c + 1] = make_ulonglong2(acc[i][2], acc[i][3]);
       }
     }
   }
@@ -360,9 +363,14 @@ static cudaError_t launch_column_sum(const float* partial, int parts, int64_t n,
 // Threads for `units` row units of 8 values, `vpt` per thread.
 static int norm_threads(int64_t units, int vpt) { return (int)(((units + vpt - 1) / vpt + 31) / 32 * 32); }
 
-// Blocks of the backward pass: one per token up to kNormBwdBlocks, which is at most four per SM.
-constexpr int kNormBwdBlocks = 2 * 148;
-static int norm_bwd_blocks(int64_t M) { return (int)(M < kNormBwdBlocks ? M : kNormBwdBlocks); }
+// Units per thread of the backward kernel, and its blocks: one per token up to what keeps about 640
+// threads per SM busy (2 to 16 blocks), then each block walks over its share of the tokens.
+static int norm_bwd_vpt(int64_t units) { return units > 1024 ? 4 : units > 64 ? 2 : 1; }
+static int norm_bwd_blocks(int64_t M, int64_t K) {
+  const int64_t units = K / 8;
+  const int64_t per_sm = std::min<int64_t>(16, std::max<int64_t>(2, 640 / norm_threads(units, norm_bwd_vpt(units))));
+  return (int)std::min<int64_t>(M, 148 * per_sm);
+}
 
 constexpr int64_t kNormUnits = 4 * 512;       // row units that one forward block's registers hold
 // Row units of which the backward's ring holds three tokens' dy, h and dh (216 KB of the 227 KB a
@@ -412,20 +420,20 @@ static cudaError_t launch_rmsnorm_bwd_v(const NormBwdArgs& a, int blocks, int th
 }
 
 static cudaError_t launch_rmsnorm_bwd(const NormBwdArgs& a, uint16_t* dweight, cudaStream_t st) {
-  const int blocks = norm_bwd_blocks(a.M);
+  const int blocks = norm_bwd_blocks(a.M, a.K);
   const int64_t units = a.K / 8;
+  const int vpt = norm_bwd_vpt(units), threads = norm_threads(units, vpt);
   cudaError_t e;
   if (units > kNormUnits) {
     rmsnorm_bwd_long_kernel<<<blocks, 512, 0, st>>>(a);
     e = cudaGetLastError();
-  } else if (units > kNormBwdUnits3) {
-    e = launch_rmsnorm_bwd_v<4, 2>(a, blocks, norm_threads(units, 4), st);
-  } else if (units > 1024) {
-    e = launch_rmsnorm_bwd_v<4, 3>(a, blocks, norm_threads(units, 4), st);
-  } else if (units > 64) {
-    e = launch_rmsnorm_bwd_v<2, 3>(a, blocks, norm_threads(units, 2), st);
+  } else if (vpt == 4) {
+    e = units > kNormBwdUnits3 ? launch_rmsnorm_bwd_v<4, 2>(a, blocks, threads, st)
+                               : launch_rmsnorm_bwd_v<4, 3>(a, blocks, threads, st);
+  } else if (vpt == 2) {
+    e = launch_rmsnorm_bwd_v<2, 3>(a, blocks, threads, st);
   } else {
-    e = launch_rmsnorm_bwd_v<1, 3>(a, blocks, norm_threads(units, 1), st);
+    e = launch_rmsnorm_bwd_v<1, 3>(a, blocks, threads, st);
   }
   if (e != cudaSuccess || !dweight) return e;
   return launch_column_sum(a.partial, blocks, a.K, dweight, st);
