@@ -764,7 +764,7 @@ int linear_fwd_impl(const uint16_t* x, const LinearShape& sh, int codebook, int 
   if (workspace_bytes < need) return fail(QNF4_ERR_WORKSPACE, "workspace needs %zu bytes", need);
   if (int rc = check_arch()) return rc;
   mark(0, st);
-  if (post && M <= qnf4::kFewTokens) {
+  if (post && qnf4::few_token_fits(M, K, N)) {
     // the workspace of the tile path holds t (M r floats) with room to spare
     float* t = A ? (t_saved ? t_saved : static_cast<float*>(workspace)) : nullptr;
     if (A) {
