@@ -22,31 +22,60 @@ enum Act : int32_t { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kAc
 constexpr float kSqrt2OverPi = 0.79788456080286536f, kSqrtHalf = 0.70710678118654752f,
                 kInvSqrt2Pi = 0.39894228040143268f, kGeluCubic = 0.044715f;
 
-// 1 / (1 + e^-v): the approximate exponential and reciprocal instructions, each within a few
-// units of the 23rd bit, far below the bf16 rounding that follows.  e^-v = inf gives 0.
-__device__ __forceinline__ float logistic(float v) {
-  float r;
-  const float d = 1.0f + __expf(-v);
-  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(d));
-  return r;
-}
-
-template <int ACT>
-__device__ __forceinline__ float act_value(float z) {
-  if constexpr (ACT == kActRelu) return z < 0.0f ? 0.0f : z;    // a NaN stays one
-  if constexpr (ACT == kActSilu) return z * logistic(z);
-  if constexpr (ACT == kActGelu) return 0.5f * z * erfcf(-kSqrtHalf * z);
-  if constexpr (ACT == kActGeluTanh) return z * logistic(2.0f * kSqrt2OverPi * (z + kGeluCubic * z * z * z));
-  return z;
-}
-
-// The same with subnormal results flushed to 0, for the slopes: one instruction each instead of a
-// range-checked sequence.  p is then 0 below 2^-126, far under the slopes' bf16 rounding.
+// 1 / (1 + e^-v) by the approximate exponential and reciprocal instructions, each within a few units
+// of the 23rd bit, far below the bf16 rounding that follows.  Subnormal results are flushed: p is 0
+// below 2^-126.
 __device__ __forceinline__ float logistic_ftz(float v) {
   float e, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(v * -1.4426950408889634f));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
   return r;
+}
+
+// Phi(-x) = erfc(x / sqrt 2) / 2 for x >= 0, two values at a time: the Chebyshev fit of Press et al.,
+// Numerical Recipes (erfcc): erfc(y) = t exp(-y^2 + P(t)), t = 1 / (1 + y / 2), of fractional error
+// below 1.2e-7 everywhere, so that the far negative tail of z Phi(z) keeps its leading bits.  (The
+// library's erfcf took three times the instructions.)
+__device__ __forceinline__ uint64_t upper_tail2(uint64_t x) {
+  const uint64_t y = f32x2_mul(x, f32_pair(kSqrtHalf, kSqrtHalf));
+  const uint64_t d = f32x2_fma(y, f32_pair(0.5f, 0.5f), f32_pair(1.0f, 1.0f));
+  float t0, t1;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t0) : "f"(pair_lo(d)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t1) : "f"(pair_hi(d)));
+  const uint64_t t = f32_pair(t0, t1);
+  uint64_t s = f32_pair(0.17087277f, 0.17087277f);
+  s = f32x2_fma(s, t, f32_pair(-0.82215223f, -0.82215223f));
+  s = f32x2_fma(s, t, f32_pair(1.48851587f, 1.48851587f));
+  s = f32x2_fma(s, t, f32_pair(-1.13520398f, -1.13520398f));
+  s = f32x2_fma(s, t, f32_pair(0.27886807f, 0.27886807f));
+  s = f32x2_fma(s, t, f32_pair(-0.18628806f, -0.18628806f));
+  s = f32x2_fma(s, t, f32_pair(0.09678418f, 0.09678418f));
+  s = f32x2_fma(s, t, f32_pair(0.37409196f, 0.37409196f));
+  s = f32x2_fma(s, t, f32_pair(1.00002368f, 1.00002368f));
+  s = f32x2_fma(s, t, f32_pair(-1.26551223f, -1.26551223f));
+  s = f32x2_fma(f32x2_mul(x, f32_pair(-0.5f, -0.5f)), x, s);    // - y^2 = - x^2 / 2
+  float e0, e1;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(pair_lo(s) * 1.4426950408889634f));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(pair_hi(s) * 1.4426950408889634f));
+  return f32x2_mul(f32x2_mul(t, f32_pair(0.5f, 0.5f)), f32_pair(e0, e1));
+}
+
+// act(z) for two values at a time
+template <int ACT>
+__device__ __forceinline__ uint64_t act_value2(uint64_t z) {
+  const float z0 = pair_lo(z), z1 = pair_hi(z);
+  if constexpr (ACT == kActRelu) return f32_pair(z0 < 0.0f ? 0.0f : z0, z1 < 0.0f ? 0.0f : z1);   // a NaN stays one
+  if constexpr (ACT == kActSilu) return f32x2_mul(z, f32_pair(logistic_ftz(z0), logistic_ftz(z1)));
+  if constexpr (ACT == kActGelu) {
+    const uint64_t s = upper_tail2(f32_pair(fabsf(z0), fabsf(z1)));
+    return f32x2_mul(z, f32_pair(z0 > 0.0f ? 1.0f - pair_lo(s) : pair_lo(s), z1 > 0.0f ? 1.0f - pair_hi(s) : pair_hi(s)));
+  }
+  if constexpr (ACT == kActGeluTanh) {
+    constexpr float c = 2.0f * kSqrt2OverPi;
+    const uint64_t v = f32x2_mul(z, f32x2_fma(f32x2_mul(z, z), f32_pair(c * kGeluCubic, c * kGeluCubic), f32_pair(c, c)));
+    return f32x2_mul(z, f32_pair(logistic_ftz(pair_lo(v)), logistic_ftz(pair_hi(v))));
+  }
+  return z;
 }
 
 // dy * act'(z) for two values at a time
@@ -101,27 +130,24 @@ __device__ __forceinline__ uint64_t act_grad2(uint64_t dy, uint64_t z) {
   return dy;
 }
 
-// act over 8 values; `act` is the same for the whole grid
-__device__ __forceinline__ void act_apply8(float (&z)[8], int act) {
+// act over n values; `act` is the same for the whole grid
+template <int ACT, int N>
+__device__ __forceinline__ void act_apply_t(float (&z)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    const uint64_t v = act_value2<ACT>(f32_pair(z[i], z[i + 1]));
+    z[i] = pair_lo(v);
+    z[i + 1] = pair_hi(v);
+  }
+}
+template <int N>
+__device__ __forceinline__ void act_apply(float (&z)[N], int act) {
   switch (act) {
-    case kActRelu:
-#pragma unroll
-      for (int i = 0; i < 8; ++i) z[i] = act_value<kActRelu>(z[i]);
-      break;
-    case kActSilu:
-#pragma unroll
-      for (int i = 0; i < 8; ++i) z[i] = act_value<kActSilu>(z[i]);
-      break;
-    case kActGelu:
-#pragma unroll
-      for (int i = 0; i < 8; ++i) z[i] = act_value<kActGelu>(z[i]);
-      break;
-    case kActGeluTanh:
-#pragma unroll
-      for (int i = 0; i < 8; ++i) z[i] = act_value<kActGeluTanh>(z[i]);
-      break;
-    default:
-      break;
+    case kActRelu: act_apply_t<kActRelu>(z); break;
+    case kActSilu: act_apply_t<kActSilu>(z); break;
+    case kActGelu: act_apply_t<kActGelu>(z); break;
+    case kActGeluTanh: act_apply_t<kActGeluTanh>(z); break;
+    default: break;
   }
 }
 
@@ -147,7 +173,7 @@ __global__ void __launch_bounds__(256) reduce_splits_epilogue_kernel(const float
     for (int j = 0; j < 8; ++j) f[j] += q[j];
   }
   if (e.z) reinterpret_cast<uint4*>(e.z)[i] = pack8(f);
-  act_apply8(f, e.act);
+  act_apply(f, e.act);
   if (e.residual) {
     unpack8(reinterpret_cast<const uint4*>(e.residual)[i], q);
 #pragma unroll

@@ -308,8 +308,8 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) few_token_kernel(const __gr
       if (p.post.bias) z += __uint_as_float((uint32_t)p.post.bias[n] << 16);
       const int64_t at = (int64_t)tok * p.N + n;
       if (p.post.z) p.post.z[at] = __bfloat16_as_ushort(__float2bfloat16_rn(z));
-      float v[8] = {z, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-      act_apply8(v, p.post.act);
+      float v[2] = {z, 0.0f};
+      act_apply(v, p.post.act);
       if (p.post.residual) v[0] += __uint_as_float((uint32_t)p.post.residual[at] << 16);
       p.y[at] = __bfloat16_as_ushort(__float2bfloat16_rn(v[0]));
     }

@@ -689,10 +689,49 @@ __global__ void __launch_bounds__(Cfg<BN, A_TMEM>::kThreads, 1) qlora_gemm_kerne
       const TileInfo ti = tile_info<BN>(p, tiles_m, tiles_n, tt);
       const int buf = (int)(tc % NB);
       const uint32_t use = (uint32_t)(tc / NB) & 1u;
-      if (!mbar_wait(&accfull[buf], use, abort_word, kErrWaitMma)) break;
-      tc_fence_after();
       const int row = ti.row0 + 32 * q + lane;
       const bool row_ok = row < p.rows;
+      // With `post` the bias and the first chunk of the residual are fetched while the tile's MMAs
+      // run, the rest of the residual is brought into L2.
+      const int fbase = ti.row0 + 32 * q + (lane & ~7);
+      float bias = 0.0f;
+      uint4 rv[4];
+      auto load_residual = [&](int c) {   // tokens c .. c + 31 of this warp's share: 8 features of token c + 8 b + lane % 8
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const int col = ti.col0 + c_base + c + 8 * b + (lane & 7);
+          rv[b] = make_uint4(0u, 0u, 0u, 0u);
+          if (c < kCols && col < p.cols && fbase < p.rows)
+            rv[b] = __ldcs(reinterpret_cast<const uint4*>(p.post.residual + (int64_t)col * p.ld_out + fbase));
+        }
+      };
+      // 32 tokens of this warp's features as bf16: 16 bytes per thread and 8 tokens
+      auto store_chunk = [&](uint16_t* out, const float (&f)[32], int c) {
+        uint32_t w[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) w[k] = pack_bf16x2(f[2 * k], f[2 * k + 1]);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          uint32_t x0 = w[4 * b], x1 = w[4 * b + 1], x2 = w[4 * b + 2], x3 = w[4 * b + 3];
+          transpose8x8_bf16(x0, x1, x2, x3, lane);
+          const int col = ti.col0 + c_base + c + 8 * b + (lane & 7);
+          if (col < p.cols && fbase < p.rows)
+            *reinterpret_cast<uint4*>(out + (int64_t)col * p.ld_out + fbase) = make_uint4(x0, x1, x2, x3);
+        }
+      };
+      if constexpr (POST) {
+        if (p.post.bias && row_ok) bias = __uint_as_float((uint32_t)p.post.bias[row] << 16);
+        if (p.post.residual && kChunk == 32) {
+          load_residual(0);
+          for (int c = 32; c < kCols; c += 8) {
+            const int col = ti.col0 + c_base + c + (lane & 7);
+            if (col < p.cols && fbase < p.rows)
+              asm volatile("prefetch.global.L2 [%0];" ::"l"(p.post.residual + (int64_t)col * p.ld_out + fbase));
+          }
+        }
+      }
+      if (!mbar_wait(&accfull[buf], use, abort_word, kErrWaitMma)) break;
+      tc_fence_after();
       const uint32_t taddr0 = tmem_base + ((uint32_t)(32 * q) << 16) + (uint32_t)(buf * C::kAccStride + c_base);
       {
 #pragma unroll 1
@@ -703,39 +742,28 @@ __global__ void __launch_bounds__(Cfg<BN, A_TMEM>::kThreads, 1) qlora_gemm_kerne
           tmem_ld_wait();
           if constexpr (kChunk == 32) {
             if constexpr (POST) {
-              // The thread's feature of 8 tokens at a time: bias, activation and residual in fp32,
-              // one rounding.  The residual arrives as the outputs leave (16 bytes of one token
-              // per thread), so the same 8 x 8 transpose brings it into the accumulator's layout.
-              const int fbase = ti.row0 + 32 * q + (lane & ~7);
-              const float bias = (p.post.bias && row_ok) ? __uint_as_float((uint32_t)p.post.bias[row] << 16) : 0.0f;
-              uint16_t* out = reinterpret_cast<uint16_t*>(p.out);
+              // The thread's feature of 32 tokens: bias, activation and residual in fp32, one
+              // rounding.  The residual arrives as the outputs leave (16 bytes of one token per
+              // thread), so the same 8 x 8 transpose brings it into the accumulator's layout.  Each
+              // part runs over the whole chunk, so that its four transposes overlap (with the
+              // parts inside a loop over 8 tokens the epilogue took 1.5 times as long).
+              float f[32];
 #pragma unroll
-              for (int b = 0; b < 4; ++b) {
-                const int col = ti.col0 + c_base + c0 + 8 * b + (lane & 7);
-                const bool ok = col < p.cols && fbase < p.rows;
-                const int64_t at = (int64_t)col * p.ld_out + fbase;
-                float f[8];
+              for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(r[j]) + bias;
+              if (p.post.z) store_chunk(p.post.z, f, c0);
+              act_apply(f, p.post.act);
+              if (p.post.residual) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(r[8 * b + j]) + bias;
-                if (p.post.z) {
-                  uint4 v = pack8(f);
-                  transpose8x8_bf16(v.x, v.y, v.z, v.w, lane);
-                  if (ok) *reinterpret_cast<uint4*>(p.post.z + at) = v;
-                }
-                act_apply8(f, p.post.act);
-                if (p.post.residual) {
-                  uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                  if (ok) v = *reinterpret_cast<const uint4*>(p.post.residual + at);
-                  transpose8x8_bf16(v.x, v.y, v.z, v.w, lane);
+                for (int b = 0; b < 4; ++b) {
+                  transpose8x8_bf16(rv[b].x, rv[b].y, rv[b].z, rv[b].w, lane);
                   float g[8];
-                  unpack8(v, g);
+                  unpack8(rv[b], g);
 #pragma unroll
-                  for (int j = 0; j < 8; ++j) f[j] += g[j];
+                  for (int j = 0; j < 8; ++j) f[8 * b + j] += g[j];
                 }
-                uint4 v = pack8(f);
-                transpose8x8_bf16(v.x, v.y, v.z, v.w, lane);
-                if (ok) *reinterpret_cast<uint4*>(out + at) = v;
+                load_residual(c0 + kChunk);   // one chunk ahead
               }
+              store_chunk(reinterpret_cast<uint16_t*>(p.out), f, c0);
               continue;
             }
             if (p.epi == kEpiBf16T) {
@@ -745,7 +773,6 @@ __global__ void __launch_bounds__(Cfg<BN, A_TMEM>::kThreads, 1) qlora_gemm_kerne
               uint32_t w[16];
 #pragma unroll
               for (int k = 0; k < 16; ++k) w[k] = pack_bf16x2(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1]));
-              const int fbase = ti.row0 + 32 * q + (lane & ~7);
               uint16_t* out = reinterpret_cast<uint16_t*>(p.out);
 #pragma unroll
               for (int b = 0; b < 4; ++b) {
@@ -761,7 +788,6 @@ __global__ void __launch_bounds__(Cfg<BN, A_TMEM>::kThreads, 1) qlora_gemm_kerne
           if (!row_ok) continue;
           if constexpr (POST) {
             // 16-token tiles: two groups of 8 tokens, scalar accesses
-            const float bias = p.post.bias ? __uint_as_float((uint32_t)p.post.bias[row] << 16) : 0.0f;
             uint16_t* out = reinterpret_cast<uint16_t*>(p.out);
 #pragma unroll
             for (int j0 = 0; j0 < kChunk; j0 += 8) {
@@ -774,7 +800,7 @@ __global__ void __launch_bounds__(Cfg<BN, A_TMEM>::kThreads, 1) qlora_gemm_kerne
                 for (int j = 0; j < 8; ++j)
                   if (col0 + j < p.cols) p.post.z[(int64_t)(col0 + j) * p.ld_out + row] = f32_to_bf16_bits(f[j]);
               }
-              act_apply8(f, p.post.act);
+              act_apply(f, p.post.act);
 #pragma unroll
               for (int j = 0; j < 8; ++j) {
                 if (col0 + j >= p.cols) continue;

@@ -836,7 +836,7 @@ int linear_fwd_impl(const uint16_t* x, const LinearShape& sh, int codebook, int 
       gp.epi = qnf4::kEpiBf16T;
       gp.out = y;
       gp.ld_out = N;
-      if (post) {
+      if (post && (post->bias || post->residual || post->z || post->act != qnf4::kActNone)) {
         gp.has_post = 1;
         gp.post = *post;
       }

@@ -296,6 +296,29 @@ def test_linear_epilogue_identity_reproduces_the_weight():
             assert np.array_equal(_bits(y), _bits(Wd.t()[K - m:].contiguous())), m
 
 
+@pytest.mark.parametrize("M,N,K,r", [(2, 128, 64, 8), (50, 136, 64, 8), (256, 128, 64, 8), (300, 200, 192, 64), (513, 264, 1000, 0), (2100, 1152, 256, 16),
+                                     (777, 136, 2048, 32)])
+def test_linear_residual_without_an_activation(M, N, K, r):
+    """With the product zero (x = 0) y is the residual itself, values that are not finite among it; ragged
+    rows and columns, K splits; with a bias too."""
+    W = _weight(N, K, 101)
+    Wd = oracle_weight(W)["w_deq"]
+    Wq = q.nf4_quantize_dq(W.cuda())
+    inp = synth.linear_inputs(M, N, K, max(r, 8), 102)
+    A, B = (inp["A"].cuda(), inp["B"].cuda()) if r else (None, None)
+    x, res, bias = inp["x"], (_normal((M, N), 3.0, 103).float() * 2.0 ** torch.arange(N).remainder(60)).to(BF), _normal((N,), 0.5, 104)
+    res[1, 5], res[M - 1, N - 1], res[M // 2, 77] = float("inf"), float("-inf"), float("nan")
+    y, _, _ = q.qlora_linear_epilogue_fwd(torch.zeros_like(x).cuda(), Wq, A, B, 0.5, residual=res.cuda())
+    assert torch.equal(torch.nan_to_num(y.cpu(), nan=3.0), torch.nan_to_num(res, nan=3.0))
+    assert torch.isnan(y).sum() == 1
+    for b in (None, bias):
+        y, t, _ = q.qlora_linear_epilogue_fwd(x.cuda(), Wq, A, B, 0.5, bias=_c(b), residual=inp["dY"].cuda(), save=True)
+        torch.cuda.synchronize()
+        assert q.check_device_error() == 0 and (t is not None) == (r > 0)
+        A_, B_ = (inp["A"], inp["B"]) if r else (None, None)
+        assert_within_tolerance(y, _epi_ref(x, Wd, A_, B_, 0.5, b, "none", inp["dY"])[0], "y")
+
+
 def test_linear_epilogue_far_tails_of_the_activations():
     """Pre-activations from -30 to 30 and infinite ones, through a one-weight layer."""
     N, K = 8, 64
