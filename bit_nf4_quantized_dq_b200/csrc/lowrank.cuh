@@ -416,16 +416,16 @@ __device__ __forceinline__ void split3(double v, uint16_t& a, uint16_t& b, uint1
   c = __bfloat16_as_ushort(__float2bfloat16_rn((float)r2));
 }
 
-// sum_z p[z * stride] for z = 0 .. splits-1, added in that order; the loads of up to eight
+// sum_z p[z * stride] for z = 0 .. splits-1, added in that order; the loads of up to sixteen
 // splits are issued before their sum, so the splits' memory latencies overlap.
 __device__ __forceinline__ double sum_splits(const double* __restrict__ p, int splits, int64_t stride) {
   double v = 0.0;
-  for (int z0 = 0; z0 < splits; z0 += 8) {
-    double x[8];
+  for (int z0 = 0; z0 < splits; z0 += 16) {
+    double x[16];
 #pragma unroll
-    for (int z = 0; z < 8; ++z) x[z] = (z0 + z < splits) ? p[(int64_t)(z0 + z) * stride] : 0.0;
+    for (int z = 0; z < 16; ++z) x[z] = (z0 + z < splits) ? p[(int64_t)(z0 + z) * stride] : 0.0;
 #pragma unroll
-    for (int z = 0; z < 8; ++z)
+    for (int z = 0; z < 16; ++z)
       if (z0 + z < splits) v += x[z];
   }
   return v;
@@ -434,15 +434,16 @@ __device__ __forceinline__ double sum_splits(const double* __restrict__ p, int s
 // Token-side result (t or u): v = alpha * sum_z partial[z][j][m].  Optional outputs:
 // fp32 [M][r]; bf16 hi / lo [M][r] (two-term split, for the fused GEMMs' adapter k-blocks);
 // the three-term split transposed, T3[term][j][m] with row pitch ldT (for dA / dB).
-// One 32 x 32 tile (m0.., j0..) per block of 32 x 8 threads: the partials are read along m,
-// the [M][r] outputs written along j through a shared-memory transpose.
+// One tile of 32 tokens x 8 columns per block of 32 x 8 threads, one element per thread (32 x 32 tiles
+// left a 512-token call with 32 blocks and 28 us, 8 us now): the partials are read along m, the
+// [M][r] outputs written along j through a shared-memory transpose.
 __global__ void finalize_tokens_kernel(const double* __restrict__ partial, int splits, int64_t M, int64_t r,
                                        double alpha, float* __restrict__ f32, uint16_t* __restrict__ hi,
                                        uint16_t* __restrict__ lo, uint16_t* __restrict__ T3, int64_t ldT) {
-  __shared__ double tile[32][33];
-  const int64_t m0 = (int64_t)blockIdx.x * 32, j0 = (int64_t)blockIdx.y * 32;
-  for (int i = threadIdx.y; i < 32; i += blockDim.y) {
-    const int64_t j = j0 + i, m = m0 + threadIdx.x;
+  __shared__ double tile[8][33];
+  const int64_t m0 = (int64_t)blockIdx.x * 32, j0 = (int64_t)blockIdx.y * 8;
+  {
+    const int64_t j = j0 + threadIdx.y, m = m0 + threadIdx.x;
     double v = 0.0;
     if (m < M && j < r) {
       v = sum_splits(partial + j * M + m, splits, r * M);
@@ -455,19 +456,18 @@ __global__ void finalize_tokens_kernel(const double* __restrict__ partial, int s
         T3[(2 * r + j) * ldT + m] = c;
       }
     }
-    tile[i][threadIdx.x] = v;
+    tile[threadIdx.y][threadIdx.x] = v;
   }
   __syncthreads();
-  for (int i = threadIdx.y; i < 32; i += blockDim.y) {
-    const int64_t m = m0 + i, j = j0 + threadIdx.x;
-    if (m >= M || j >= r) continue;
-    const double v = tile[threadIdx.x][i];
-    if (f32) f32[m * r + j] = (float)v;
-    if (hi) {
-      const __nv_bfloat16 h = __float2bfloat16_rn((float)v);
-      hi[m * r + j] = __bfloat16_as_ushort(h);
-      lo[m * r + j] = bf16_bits_rn(v - (double)__bfloat162float(h));
-    }
+  const int t = threadIdx.y * 32 + threadIdx.x;
+  const int64_t m = m0 + (t >> 3), j = j0 + (t & 7);
+  if (m >= M || j >= r) return;
+  const double v = tile[t & 7][t >> 3];
+  if (f32) f32[m * r + j] = (float)v;
+  if (hi) {
+    const __nv_bfloat16 h = __float2bfloat16_rn((float)v);
+    hi[m * r + j] = __bfloat16_as_ushort(h);
+    lo[m * r + j] = bf16_bits_rn(v - (double)__bfloat162float(h));
   }
 }
 
@@ -494,35 +494,34 @@ __global__ void split3_T_kernel(const float* __restrict__ t, int64_t M, int64_t 
 }
 
 // Feature-side gradient: g[j][i] = bf16(sum_z partial[z][j][i]); transpose_out = 0 writes
-// out[j * n + i] (dA, [r][K]), 1 writes out[i * r + j] (dB, [N][r]).  One 32 x 32 tile
-// (i0.., j0..) per block of 32 x 8 threads; the transposed case goes through shared memory so
-// that both the partials and the output are accessed along their rows.
+// out[j * n + i] (dA, [r][K]), 1 writes out[i * r + j] (dB, [N][r]).  One tile of 32 rows x 8 columns
+// (i0.., j0..) per block of 32 x 8 threads; the transposed case goes through shared memory so that
+// both the partials and the output are accessed along their rows.
 __global__ void finalize_grad_kernel(const double* __restrict__ partial, int splits, int64_t r, int64_t n,
                                      uint16_t* __restrict__ out, int transpose_out) {
-  __shared__ uint16_t tile[32][34];
-  const int64_t i0 = (int64_t)blockIdx.x * 32, j0 = (int64_t)blockIdx.y * 32;
-  for (int a = threadIdx.y; a < 32; a += blockDim.y) {
-    const int64_t j = j0 + a, i = i0 + threadIdx.x;
+  __shared__ uint16_t tile[8][34];
+  const int64_t i0 = (int64_t)blockIdx.x * 32, j0 = (int64_t)blockIdx.y * 8;
+  {
+    const int64_t j = j0 + threadIdx.y, i = i0 + threadIdx.x;
     uint16_t g = 0;
     if (i < n && j < r) {
       const double v = sum_splits(partial + j * n + i, splits, r * n);
       g = bf16_bits_rn(v);
       if (!transpose_out) out[j * n + i] = g;
     }
-    tile[a][threadIdx.x] = g;
+    tile[threadIdx.y][threadIdx.x] = g;
   }
   if (!transpose_out) return;
   __syncthreads();
-  for (int a = threadIdx.y; a < 32; a += blockDim.y) {
-    const int64_t i = i0 + a, j = j0 + threadIdx.x;
-    if (i < n && j < r) out[i * r + j] = tile[threadIdx.x][a];
-  }
+  const int t = threadIdx.y * 32 + threadIdx.x;
+  const int64_t i = i0 + (t >> 3), j = j0 + (t & 7);
+  if (i < n && j < r) out[i * r + j] = tile[t & 7][t >> 3];
 }
 
 static cudaError_t launch_finalize_tokens(const double* partial, int splits, int64_t M, int64_t r, double alpha,
                                           float* f32, uint16_t* hi, uint16_t* lo, uint16_t* T3, int64_t ldT,
                                           cudaStream_t st) {
-  dim3 grid((unsigned)((M + 31) / 32), (unsigned)((r + 31) / 32));
+  dim3 grid((unsigned)((M + 31) / 32), (unsigned)((r + 7) / 8));
   finalize_tokens_kernel<<<grid, dim3(32, 8), 0, st>>>(partial, splits, M, r, alpha, f32, hi, lo, T3, ldT);
   return cudaGetLastError();
 }
@@ -536,7 +535,7 @@ static cudaError_t launch_split3_T(const float* t, int64_t M, int64_t r, uint16_
 
 static cudaError_t launch_finalize_grad(const double* partial, int splits, int64_t r, int64_t n, uint16_t* out,
                                         int transpose_out, cudaStream_t st) {
-  dim3 grid((unsigned)((n + 31) / 32), (unsigned)((r + 31) / 32));
+  dim3 grid((unsigned)((n + 31) / 32), (unsigned)((r + 7) / 8));
   finalize_grad_kernel<<<grid, dim3(32, 8), 0, st>>>(partial, splits, r, n, out, transpose_out);
   return cudaGetLastError();
 }
