@@ -159,36 +159,38 @@ __device__ __forceinline__ void a8_decode16(const uint4& q, uint32_t byte, uint3
   }
 }
 
-// Threads (x along the features, 8 each; y along the tokens); each takes kA8Rows tokens and loads
-// all of them first, so that enough bytes are in flight.  blockDim.x is a multiple of 4, so a group's
-// four lanes sit in one warp and in one row.
+// Threads (x along the features, 8 each; y along the tokens); each takes kA8Rows tokens at a time,
+// `batches` times, and loads all of them first, so that enough bytes are in flight.  blockDim.x is a
+// multiple of 4, so a group's four lanes sit in one warp and in one row.
 constexpr int kA8Rows = 4;
 
 __global__ void __launch_bounds__(256) act8_quantize_kernel(const uint16_t* __restrict__ x, int64_t M, int64_t K,
-                                                            uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+                                                            int batches, uint8_t* __restrict__ codes,
+                                                            uint8_t* __restrict__ scales) {
   const int64_t ld = a8_ld(K), G = a8_groups(K);
-  const int64_t m0 = (int64_t)blockIdx.x * blockDim.y * kA8Rows + threadIdx.y;
-  const int by = (int)blockDim.y;
-  const int rows = (int)min(M - m0, (int64_t)kA8Rows * by);   // row i of this thread exists while i * by < rows
+  const int by = (int)blockDim.y, per_block = kA8Rows * by * batches;
+  const int64_t m0 = (int64_t)blockIdx.x * per_block + threadIdx.y;
+  const int rows = (int)min(M - m0, (int64_t)(per_block - threadIdx.y));   // tokens m0, m0 + by, ... below m0 + rows
   for (int64_t c0 = (int64_t)blockIdx.y * blockDim.x; c0 < 4 * G; c0 += (int64_t)gridDim.y * blockDim.x) {
     const int64_t k = 8 * (c0 + threadIdx.x);
     const uint16_t* src = x + m0 * K + k;
-    uint4 v[kA8Rows];
-    const int in = k < K ? rows : 0;
-#pragma unroll
-    for (int i = 0; i < kA8Rows; ++i, src += by * K) {
-      v[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (i * by < in) v[i] = __ldcs(reinterpret_cast<const uint4*>(src));
-    }
-    const int out = k < ld ? rows : 0, mark = (threadIdx.x & 3) == 0 ? in : 0;
     uint8_t* dst = codes + m0 * ld + k;
     uint8_t* sdst = scales + m0 * G + (k >> 5);
+    const int in = k < K ? rows : 0, out = k < ld ? rows : 0, mark = (threadIdx.x & 3) == 0 ? in : 0;
+    for (int r = 0; r < per_block; r += kA8Rows * by) {
+      uint4 v[kA8Rows];
 #pragma unroll
-    for (int i = 0; i < kA8Rows; ++i, dst += by * ld, sdst += by * G) {
-      uint2 q;
-      const uint32_t byte = a8_encode8(v[i], q);
-      if (i * by < out) *reinterpret_cast<uint2*>(dst) = q;
-      if (i * by < mark) *sdst = (uint8_t)byte;
+      for (int i = 0; i < kA8Rows; ++i, src += by * K) {
+        v[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (r + i * by < in) v[i] = __ldcs(reinterpret_cast<const uint4*>(src));
+      }
+#pragma unroll
+      for (int i = 0; i < kA8Rows; ++i, dst += by * ld, sdst += by * G) {
+        uint2 q;
+        const uint32_t byte = a8_encode8(v[i], q);
+        if (r + i * by < out) *reinterpret_cast<uint2*>(dst) = q;
+        if (r + i * by < mark) *sdst = (uint8_t)byte;
+      }
     }
   }
 }
@@ -224,21 +226,30 @@ __global__ void __launch_bounds__(256) act8_dequant_kernel(const uint8_t* __rest
 
 // Block shape of a kernel whose threads take 8 features each of rows of `chunks` such units: as
 // many threads along the row as it has units (a power of two, 4 .. 256), the rest along tokens.
-static void a8_launch_shape(int64_t M, int64_t chunks, dim3* grid, dim3* block) {
+static void a8_launch_shape(int64_t M, int64_t chunks, dim3* grid, dim3* block, int* batches = nullptr) {
   int bx = 4;
   while (bx < 256 && bx < chunks) bx *= 2;
   const int by = 256 / bx;
   *block = dim3((unsigned)bx, (unsigned)by);
   int64_t gy = (chunks + bx - 1) / bx;
   if (gy > 65535) gy = 65535;
-  *grid = dim3((unsigned)((M + kA8Rows * by - 1) / (kA8Rows * by)), (unsigned)gy);
+  int64_t gx = (M + kA8Rows * by - 1) / (kA8Rows * by);
+  if (batches) {   // up to four batches per block while the grid keeps eight blocks per SM
+    *batches = 1;
+    while (*batches < 4 && gx * gy >= 2 * 8 * 148) {
+      *batches *= 2;
+      gx = (M + kA8Rows * by * *batches - 1) / (kA8Rows * by * *batches);
+    }
+  }
+  *grid = dim3((unsigned)gx, (unsigned)gy);
 }
 
 static cudaError_t launch_act8_quantize(const uint16_t* x, int64_t M, int64_t K, uint8_t* codes, uint8_t* scales,
                                         cudaStream_t st) {
   dim3 grid, block;
-  a8_launch_shape(M, 4 * a8_groups(K), &grid, &block);
-  act8_quantize_kernel<<<grid, block, 0, st>>>(x, M, K, codes, scales);
+  int batches;
+  a8_launch_shape(M, 4 * a8_groups(K), &grid, &block, &batches);
+  act8_quantize_kernel<<<grid, block, 0, st>>>(x, M, K, batches, codes, scales);
   return cudaGetLastError();
 }
 
