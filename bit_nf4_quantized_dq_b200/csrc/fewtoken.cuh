@@ -8,18 +8,25 @@
 // that a warp's 64-bit reads never share a bank, and the address is one byte permute.  The pair is
 // then scaled and rounded by paired arithmetic, bf16(fp32(level * scale)), exactly the dequantized
 // weight of every other path.
-//  - One block of 16 warps per SM (the table is 64 KB).  A tile is 8 rows of W, the n side of the
-//    warp-level m16n8k16 bf16 product (fp32 sums), with up to 16 tokens on its m side.  A work item
-//    is 8 rows x 256 columns: lane (g, c) holds row g, columns 64 c .. 64 c + 63, whole blocks with
-//    one scale each; the order of the columns inside a product is free as long as x follows it.
-//  - A block's share of the tiles makes one list of items, columns outermost, cut evenly over its
-//    warps: a warp keeps the x of its 256 columns in registers and walks down the tiles.  Each
+//  - One block of 16 warps per SM (the table is 64 KB).  A work item is 16 rows of W (the m side of the
+//    warp-level m16n8k16 bf16 product, fp32 sums, with 8 or 16 tokens on its n side) x 256 columns:
+//    lane (g, c) holds rows g and g + 8, columns 64 c .. 64 c + 63, whole blocks with one scale each;
+//    the order of the columns inside a product is free as long as x follows it.
+//  - A block's share of the 16-row tiles makes one list of items, columns outermost, cut evenly over
+//    its warps: a warp keeps the x of its 256 columns in registers and walks down the tiles.  Each
 //    item's sums go to shared memory and are added over the columns in order, so results do not
 //    depend on timing; the epilogue is applied there.
-//  - The codes and scales of the next two items are on their way while one is expanded.
+//  - The codes come by TMA, 2 KB per item, three items ahead in a ring of each warp: 96 KB on their way
+//    per SM.  (With 2 KB ahead in a thread's registers or 48 KB in all, the stream alone took 9 us
+//    more than an empty loop, at 36 MB.)  The 128-byte swizzle lets the lanes read them without bank
+//    conflicts.  The scales are one item ahead in registers.
 //  - tcgen05 would need the tile staged for 128 rows and at least 16 tokens; as 16-token tiles of the
-//    fused GEMM (with its K splits and a reduction) the same layer takes 52 us, here 24 us.
+//    fused GEMM (with its K splits and a reduction) the same layer takes 52 us.
+// With K % 64 != 0 code rows are only 4-byte aligned and blocks span rows: a kernel of its own reads
+// the codes into registers, in tiles of 8 rows.
 #pragma once
+
+#include <algorithm>
 
 #include "epilogue.cuh"
 #include "gemm.h"
@@ -27,19 +34,23 @@
 namespace qnf4 {
 
 constexpr int kFewTokens = 16;    // most tokens of this path
-constexpr int kFewRows = 8;       // rows of W per tile
 constexpr int kFewCols = 256;     // columns per work item
 constexpr int kFewWarps = 16;
-// The table sits at shared address 65536, so that its address bytes are (lane * 8, code byte, 1, 0):
-// one permute of the codes and a lane constant.  The items' sums lie behind it.
-constexpr uint32_t kFewTableAddr = 65536, kFewTableBytes = 65536;
-constexpr int kFewSumBytes = 96 * 1024;
-constexpr int kFewSmemBytes = (int)(kFewTableAddr + kFewTableBytes) + kFewSumBytes;
+// Shared memory.  The table sits at shared address 65536, so that its address bytes are (lane * 8, code
+// byte, 1, 0): one permute of the codes and a lane constant.  The items' sums lie in front of it, from
+// the start of the block's part on, the warps' rings of codes behind it.
+constexpr uint32_t kFewTableAddr = 65536, kFewRingAddr = 131072;
+constexpr int kFewRing = 3;       // items on their way per warp
+constexpr int kFewItemBytes = 16 * kFewCols / 2;
+constexpr int kFewRingBytes = kFewWarps * kFewRing * kFewItemBytes;
+constexpr int kFewSmemBytes = (int)kFewRingAddr + kFewRingBytes + kFewWarps * kFewRing * 8 + 16;
 static_assert(kFewSmemBytes <= 227 * 1024, "shared memory of one block");
-// item sums that fit: kFewRows x (8 or 16 tokens) floats each
-__host__ __device__ constexpr int few_slots(bool two) { return kFewSumBytes / ((two ? 16 : 8) * kFewRows * 4); }
+constexpr int kFewRaggedSmemBytes = (int)kFewRingAddr;
+// Bytes of sums that every launch has room for (the block's part starts at most 2 KB up).
+constexpr int kFewSumBytes = 62 * 1024;
 
 struct FewTokenParams {
+  CUtensorMap map;         // codes [N][K / 2], boxes of 16 rows x 128 bytes, 128-byte swizzle (K % 64 == 0)
   const uint16_t* x;       // [M][K]
   int32_t M;
   int64_t K, N;
@@ -119,160 +130,388 @@ __device__ __forceinline__ void split_bf16x2(float a, float b, uint32_t& hi, uin
   lo = pack_bf16x2(a - bf_lo(hi), b - bf_hi(hi));
 }
 
-// One row's 64 columns as fetched, nothing computed yet (a use of a loaded value would hold the warp
-// until it arrives): the codes, the stored scale of their block and, where a block boundary lies
-// inside (K % 64 != 0), the next block's and the number of 8-code words before the boundary.
+// The stored scale of a block as fetched, nothing computed yet (a use of a loaded value would hold
+// the warp until it arrives).
 struct FewScale {
   uint32_t code;   // E4M3 scale code (double quantization)
   float value;     // its group constant, or the fp32 scale itself
 };
-template <bool GENERIC>
-struct FewUnit {
-  uint32_t w[8];
-  FewScale s0, s1;
-  int32_t split;
-};
-
 __device__ __forceinline__ FewScale few_scale(const FewTokenParams& p, uint32_t blk) {
   if (p.scale_fp32) return FewScale{0u, __ldg(p.scales + blk)};
   return FewScale{__ldg(p.scale_codes + blk), __ldg(p.scales + (blk >> 8))};
 }
+__device__ __forceinline__ float few_scale_value(const FewTokenParams& p, const FewScale& s, float mean) {
+  return p.scale_fp32 ? s.value : dq_block_scale(s.code, s.value, mean);
+}
 
-// `src` addresses the unit's codes, `blk` is its first block, `in_blk` the words of its first block
-// (8 where K % 64 == 0), `valid` its number of 8-code words before K.  Columns past K take codes
-// before them: x is zero there.
-template <bool GENERIC>
-__device__ __forceinline__ void few_fetch(const FewTokenParams& p, const uint8_t* src, uint32_t blk, int in_blk,
-                                          int valid, FewUnit<GENERIC>& u) {
-  u.s0 = few_scale(p, blk);
-  if constexpr (GENERIC) {
-    u.split = in_blk;
-    u.s1 = few_scale(p, in_blk < valid ? blk + 1 : blk);   // the next block exists where a valid word lies in it
+// Fills the table: warp w writes the pairs of the bytes w, w + kFewWarps, ...; `stage` holds 16 floats
+// that nothing else uses yet.  Returns the lane's table address, which every lookup's address
+// depends on (opaque, so that no lookup moves in front of the barrier).
+__device__ __forceinline__ uint32_t few_fill_table(const FewTokenParams& p, uint8_t* table, float* stage) {
+  const int lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) u.w[j] = __ldg(reinterpret_cast<const uint32_t*>(src) + (j < valid ? j : 0));
-  } else {
-    const uint4 a = __ldg(reinterpret_cast<const uint4*>(src)), b = __ldg(reinterpret_cast<const uint4*>(src) + 1);
-    u.w[0] = a.x; u.w[1] = a.y; u.w[2] = a.z; u.w[3] = a.w;
-    u.w[4] = b.x; u.w[5] = b.y; u.w[6] = b.z; u.w[7] = b.w;
+    for (int j = 0; j < 16; ++j) stage[j] = p.cb.q[j];
+  }
+  __syncthreads();
+  for (int b = threadIdx.x >> 5; b < 256; b += kFewWarps)
+    *reinterpret_cast<float2*>(table + b * 256 + lane * 8) = make_float2(stage[b & 15], stage[b >> 4]);
+  __syncthreads();
+  uint32_t lane_addr = kFewTableAddr + (uint32_t)lane * 8u;
+  asm volatile("" : "+r"(lane_addr)::"memory");
+  return lane_addr;
+}
+// Eight codes -> four bf16 pairs of the dequantized weight.
+__device__ __forceinline__ void few_expand8(uint32_t w, float scale, uint32_t lane_addr, uint32_t (&o)[4]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t at = prmt(w, lane_addr, 0x7604u | ((uint32_t)k << 4));
+    uint64_t q;
+    asm("ld.shared.b64 %0, [%1];" : "=l"(q) : "r"(at));   // the table does not change any more
+    q = f32x2_mul(q, f32_pair(scale, scale));
+    o[k] = pack_bf16x2(pair_lo(q), pair_hi(q));
   }
 }
 
-// TWO: more than 8 tokens.
-template <bool TWO, bool GENERIC>
-__global__ void __launch_bounds__(32 * kFewWarps, 1) few_token_kernel(const __grid_constant__ FewTokenParams p) {
-  constexpr int kTok = TWO ? 16 : 8;
-  constexpr int kSlot = kTok * kFewRows;
-  extern __shared__ __align__(16) uint8_t few_smem[];
-  uint8_t* const at65536 = few_smem + (kFewTableAddr - smem_u32(few_smem));
-  float* sums = reinterpret_cast<float*>(at65536 + kFewTableBytes);      // [tile][quad][kTok][kFewRows]
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
-  const float mean = p.scale_fp32 ? 0.0f : __ldg(p.mean);
-  const int quads = (int)((p.K + kFewCols - 1) / kFewCols);
-  const int64_t tiles = p.N / kFewRows;
-  const int64_t t_begin = tiles * blockIdx.x / gridDim.x, t_end = tiles * (blockIdx.x + 1) / gridDim.x;
-  // rounds of tiles whose sums fit, of even sizes
-  const int most = few_slots(TWO) / (quads + 1);
-  const int rounds = (int)((t_end - t_begin + most - 1) / most);
-  const int per_round = (int)((t_end - t_begin + rounds - 1) / rounds);
-  const uint16_t* x0 = p.x + (int64_t)min(g, p.M - 1) * p.K;       // rows past M repeat the last one, unread
-  const uint16_t* x1 = p.x + (int64_t)min(g + 8, p.M - 1) * p.K;
+// A block's share of `tiles`, and its rounds of even sizes whose sums (`slot` floats per item, `quads`
+// items per tile and one more for the adapter term) fit between `sums` and the table.
+struct FewShare {
+  int begin, end, per_round;
+};
+__device__ __forceinline__ FewShare few_share(const float* sums, int tiles, int quads, int slot) {
+  const int base = tiles / (int)gridDim.x, extra = tiles - base * (int)gridDim.x;
+  FewShare s;
+  s.begin = (int)blockIdx.x * base + min((int)blockIdx.x, extra);
+  s.end = s.begin + base + ((int)blockIdx.x < extra ? 1 : 0);
+  const int most = (int)(kFewTableAddr - smem_u32(sums)) / (4 * slot * (quads + 1));
+  const int rounds = (s.end - s.begin + most - 1) / most;
+  s.per_round = (s.end - s.begin + rounds - 1) / rounds;
+  return s;
+}
 
-  if (threadIdx.x == 0) {
-#pragma unroll
-    for (int j = 0; j < 16; ++j) sums[j] = p.cb.q[j];
+// The outputs of a round's tiles: the items' sums added over the columns in order (and the adapter
+// term, in slot nt * quads + tile), bias, activation, residual.  `at(row, token)` is a sum's place in
+// its slot.
+template <int ROWS, class At>
+__device__ __forceinline__ void few_finish(const FewTokenParams& p, const float* sums, int slot, int t0, int nt, int quads,
+                                           At at) {
+  for (int o = threadIdx.x; o < nt * ROWS * p.M; o += 32 * kFewWarps) {
+    const int row = o % ROWS, rest = o / ROWS, tl = rest % nt, tok = rest / nt;
+    const int64_t n = (int64_t)(t0 + tl) * ROWS + row;
+    if (n >= p.N) continue;
+    const float* part = sums + at(row, tok);
+    float z = 0.0f;
+#pragma unroll 8
+    for (int w = 0; w < quads; ++w) z += part[(tl * quads + w) * slot];
+    if (p.t) z += part[(nt * quads + tl) * slot];
+    if (p.post.bias) z += __uint_as_float((uint32_t)p.post.bias[n] << 16);
+    const int64_t to = (int64_t)tok * p.N + n;
+    if (p.post.z) p.post.z[to] = __bfloat16_as_ushort(__float2bfloat16_rn(z));
+    float v[2] = {z, 0.0f};
+    act_apply(v, p.post.act);
+    if (p.post.residual) v[0] += __uint_as_float((uint32_t)p.post.residual[to] << 16);
+    p.y[to] = __bfloat16_as_ushort(__float2bfloat16_rn(v[0]));
   }
-  __syncthreads();
-  for (int b = warp; b < 256; b += kFewWarps)
-    *reinterpret_cast<float2*>(at65536 + b * 256 + lane * 8) = make_float2(sums[b & 15], sums[b >> 4]);
-  __syncthreads();
-  // behind the barrier, and opaque: every lookup's address depends on it
-  uint32_t lane_addr = kFewTableAddr + (uint32_t)lane * 8u;
-  asm volatile("" : "+r"(lane_addr)::"memory");
+}
 
-  for (int64_t t0 = t_begin; t0 < t_end; t0 += per_round) {
-    const int nt = (int)min(t_end - t0, (int64_t)per_round);
+// K % 64 == 0.  TWO: more than 8 tokens.
+template <bool TWO>
+__global__ void __launch_bounds__(32 * kFewWarps, 1) few_token_kernel(const __grid_constant__ FewTokenParams p) {
+  constexpr int kRows = 16, NT = TWO ? 2 : 1, kSlot = NT * kRows * 8;   // sums [group of 8 tokens][row][token]
+  extern __shared__ __align__(16) uint8_t few_smem[];
+  uint8_t* const smem0 = few_smem - smem_u32(few_smem);                // shared address 0
+  float* const sums = reinterpret_cast<float*>(few_smem);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
+  uint8_t* const ring = smem0 + kFewRingAddr + warp * kFewRing * kFewItemBytes;
+  uint64_t* const bars = reinterpret_cast<uint64_t*>(smem0 + kFewRingAddr + kFewRingBytes);
+  uint64_t* const full = bars + warp * kFewRing;
+  volatile uint32_t* const abort_word = reinterpret_cast<uint32_t*>(bars + kFewWarps * kFewRing);
+  if (threadIdx.x < kFewWarps * kFewRing) mbar_init(&bars[threadIdx.x], 1);
+  if (threadIdx.x == 0) {
+    *abort_word = 0u;
+    tma_prefetch_desc(&p.map);
+  }
+  mbar_fence_init();
+  __syncthreads();
+
+  const int quads = (int)((p.K + kFewCols - 1) / kFewCols);
+  const FewShare share = few_share(sums, (int)((p.N + kRows - 1) / kRows), quads, kSlot);
+  const float mean = p.scale_fp32 ? 0.0f : __ldg(p.mean);
+  uint32_t lane_addr = 0u;
+  int slot = 0, pending = 0;     // the ring's slot read next, and its loads on their way
+  uint32_t phase = 0u;
+  bool ok = true;
+  for (int t0 = share.begin; t0 < share.end; t0 += share.per_round) {
+    const int nt = min(share.end - t0, share.per_round);
     const int items = nt * quads;
-    const int i0 = (int)((int64_t)items * warp / kFewWarps), i1 = (int)((int64_t)items * (warp + 1) / kFewWarps);
-    // the item whose codes are fetched next
-    int f_quad = i0 / nt, f_tile = i0 - f_quad * nt, f_valid = 0, f_in = 8;
-    const uint8_t* f_src = nullptr;
-    uint32_t f_blk = 0;
-    int64_t f_at = 0;   // flat index of the unit's first weight
-    auto locate = [&]() {
-      f_src = p.codes + (f_at >> 1);
-      f_blk = (uint32_t)(f_at >> 6);
-      f_in = GENERIC ? (int)((64 - (f_at & 63)) >> 3) : 8;
-    };
-    auto place = [&]() {
-      int64_t kcol = (int64_t)f_quad * kFewCols + 64 * c;
-      f_valid = kcol >= p.K ? 0 : (int)min((p.K - kcol) >> 3, (int64_t)8);
-      if (f_valid == 0) kcol = p.K - 8 * (f_valid = GENERIC ? 1 : 8);
-      f_at = ((t0 + f_tile) * kFewRows + g) * p.K + kcol;
-      locate();
-    };
-    auto fetch = [&](FewUnit<GENERIC>& u) {
-      few_fetch<GENERIC>(p, f_src, f_blk, f_in, f_valid, u);
-      if (++f_tile == nt) {
-        f_tile = 0;
-        if (++f_quad < quads) place();
-      } else if constexpr (GENERIC) {
-        f_at += kFewRows * p.K;
-        locate();
-      } else {
-        f_src += kFewRows / 2 * p.K;
-        f_blk += (uint32_t)(p.K >> 3);   // 8 rows of K / 64 blocks
+    const int i0 = items * warp / kFewWarps, i1 = items * (warp + 1) / kFewWarps;
+    int quad = i0 / nt, tile = i0 - quad * nt;
+    // the item whose codes are loaded next
+    int c_quad = quad, c_tile = tile, c_left = i1 - i0;
+    auto load_codes = [&](int s) {
+      if (c_left == 0) return;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&full[s], kFewItemBytes);
+        tma_load_2d(ring + s * kFewItemBytes, &p.map, c_quad * (kFewCols / 2), (t0 + c_tile) * kRows, &full[s]);
+      }
+      --c_left;
+      ++pending;
+      if (++c_tile == nt) {
+        c_tile = 0;
+        ++c_quad;
       }
     };
-    int quad = f_quad, tile = f_tile;
-    FewUnit<GENERIC> u0, u1;
+    for (int k = 0, s = slot; k < kFewRing; ++k, s = s + 1 == kFewRing ? 0 : s + 1) load_codes(s);
+    // The scales of the next item.  Columns past K (whose codes arrive as zeros, and where x is zero) and
+    // rows past N (N is a multiple of 8; their sums are not used) take the scales before them.
+    int f_quad = quad, f_tile = tile;
+    uint32_t f_blk[2] = {0u, 0u};
+    auto place = [&]() {
+      const int64_t col = min((int64_t)f_quad * kFewCols + 64 * c, p.K - 64);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int64_t n = (int64_t)(t0 + f_tile) * kRows + g + 8 * h;
+        f_blk[h] = (uint32_t)((min(n, p.N - 1) * p.K + col) >> 6);
+      }
+    };
+    FewScale next[2];
+    auto fetch = [&]() {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) next[h] = few_scale(p, f_blk[h]);
+      ++f_tile;
+      if (f_tile == nt) {
+        f_tile = 0;
+        ++f_quad;
+      }
+      if (f_tile == 0 || f_tile == nt - 1) {   // (the last tile's second half may lie past N)
+        place();
+      } else {
+        f_blk[0] += (uint32_t)(p.K >> 2);      // 16 rows of K / 64 blocks
+        f_blk[1] += (uint32_t)(p.K >> 2);
+      }
+    };
     if (i0 < i1) {
       place();
-      fetch(u0);
+      fetch();
     }
-    if (i0 + 1 < i1) fetch(u1);
+    uint4 xv[NT][8];
+    auto load_x = [&]() {   // this lane's 64 columns of its tokens; tokens past M repeat the last one, unread
+      const int64_t col = (int64_t)quad * kFewCols + 64 * c;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const uint4* src = reinterpret_cast<const uint4*>(p.x + (int64_t)min(8 * t + g, p.M - 1) * p.K + col);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) xv[t][j] = col < p.K ? __ldg(src + j) : make_uint4(0u, 0u, 0u, 0u);
+      }
+    };
+    if (i0 < i1) load_x();
+    if (lane_addr == 0u) lane_addr = few_fill_table(p, smem0 + kFewTableAddr, sums);   // while the codes arrive
+    for (int i = i0; i < i1 && ok;) {
+      // this warp's tiles of one quad of columns
+      const int stop = min(i1, i + nt - tile);
+      float* out = sums + (tile * quads + quad) * kSlot + g * 8 + 2 * c;
+      for (; i < stop; ++i, out += quads * kSlot) {
+        const FewScale s0 = next[0], s1 = next[1];
+        if (i + 1 < i1) fetch();
+        if (!mbar_try_wait(&full[slot], phase) && !mbar_wait_thread(&full[slot], phase, abort_word, kErrWaitTma)) ok = false;
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        // rows g and g + 8: their 16-byte chunks 2 c and 2 c + 1 lie at (chunk ^ g), a phase of 8 lanes (two
+        // rows) reads 8 different bank groups
+        const uint8_t* row = ring + slot * kFewItemBytes + g * 128;
+        const float v0 = few_scale_value(p, s0, mean), v1 = few_scale_value(p, s1, mean);
+        float acc[NT][2][4];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[t][0][k] = acc[t][1][k] = 0.0f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint4 qa = *reinterpret_cast<const uint4*>(row + (((2 * c + h) ^ g) << 4));
+          const uint4 qb = *reinterpret_cast<const uint4*>(row + 1024 + (((2 * c + h) ^ g) << 4));
+          const uint32_t wa[4] = {qa.x, qa.y, qa.z, qa.w}, wb[4] = {qb.x, qb.y, qb.z, qb.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t a[4], b[4];
+            few_expand8(wa[j], v0, lane_addr, a);
+            few_expand8(wb[j], v1, lane_addr, b);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              const uint4& x = xv[t][4 * h + j];
+              mma_bf16_16816(acc[t][0], a[0], b[0], a[1], b[1], x.x, x.y);
+              mma_bf16_16816(acc[t][1], a[2], b[2], a[3], b[3], x.z, x.w);
+            }
+          }
+        }
+        --pending;
+        __syncwarp();   // every lane has used its codes: the slot takes the item kFewRing ahead
+        load_codes(slot);
+        if (++slot == kFewRing) {
+          slot = 0;
+          phase ^= 1u;
+        }
+        // sums of rows g and g + 8, tokens 2 c and 2 c + 1 of each group
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          *reinterpret_cast<float2*>(out + t * 128) = make_float2(acc[t][0][0] + acc[t][1][0], acc[t][0][1] + acc[t][1][1]);
+          *reinterpret_cast<float2*>(out + t * 128 + 64) =
+              make_float2(acc[t][0][2] + acc[t][1][2], acc[t][0][3] + acc[t][1][3]);
+        }
+      }
+      ++quad;
+      tile = 0;
+      if (i < i1) load_x();
+    }
+    if (p.t) {
+      // t B^T: t as bf16 hi + lo (16 significant bits), one more slot of sums per tile
+      asm volatile("griddepcontrol.wait;" ::: "memory");   // t comes from the grid before
+      for (int tl = warp; tl < nt; tl += kFewWarps) {
+        const int64_t n0 = (int64_t)(t0 + tl) * kRows + g, n1 = min(n0 + 8, p.N - 1);
+        float acc[NT][4];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[t][k] = 0.0f;
+        for (int j = 4 * c; j < p.r + 4 * c; j += 16) {   // 16 rank columns a step: lane c takes 4 of them
+          uint2 b0 = make_uint2(0u, 0u), b1 = b0;
+          if (j < p.r) {
+            b0 = __ldg(reinterpret_cast<const uint2*>(p.B + n0 * p.r + j));
+            b1 = __ldg(reinterpret_cast<const uint2*>(p.B + n1 * p.r + j));
+          }
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            float4 tv = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (j < p.r) tv = *reinterpret_cast<const float4*>(p.t + (int64_t)min(8 * t + g, p.M - 1) * p.r + j);
+            uint32_t h0, l0, h1, l1;
+            split_bf16x2(tv.x, tv.y, h0, l0);
+            split_bf16x2(tv.z, tv.w, h1, l1);
+            mma_bf16_16816(acc[t], b0.x, b1.x, b0.y, b1.y, h0, h1);
+            mma_bf16_16816(acc[t], b0.x, b1.x, b0.y, b1.y, l0, l1);
+          }
+        }
+        float* out = sums + (nt * quads + tl) * kSlot + g * 8 + 2 * c;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          *reinterpret_cast<float2*>(out + t * 128) = make_float2(acc[t][0], acc[t][1]);
+          *reinterpret_cast<float2*>(out + t * 128 + 64) = make_float2(acc[t][2], acc[t][3]);
+        }
+      }
+    }
+    __syncthreads();
+    if (*abort_word) break;   // the same for every thread: all waits of the round are over
+    few_finish<kRows>(p, sums, kSlot, t0, nt, quads, [](int row, int tok) { return (tok >> 3) * 128 + row * 8 + (tok & 7); });
+    __syncthreads();          // the sums are free for the next round
+  }
+  if (*abort_word && lane == 0) {
+    // a wait ran out: let the copies in flight land before the block's shared memory goes away
+    for (int k = 0; k < pending; ++k) {
+      const int s = slot + k < kFewRing ? slot + k : slot + k - kFewRing;
+      const uint32_t ph = slot + k < kFewRing ? phase : phase ^ 1u;
+      for (int i = 0; i < (1 << 20) && !mbar_try_wait(&full[s], ph); ++i) {}
+    }
+  }
+}
+
+// K % 64 != 0: what a lane holds of its row's 64 columns in the next item.
+struct FewUnit {
+  FewScale s0, s1;   // of the block of its first column and of the next
+  int32_t split;     // 8-code words before the boundary between them
+  uint32_t w[8];
+};
+
+// K % 64 != 0.  Tiles of 8 rows on the n side of the product, the tokens on its m side; lane (g, c) holds
+// row g, columns 64 c .. 64 c + 63.  TWO: more than 8 tokens.
+template <bool TWO>
+__global__ void __launch_bounds__(32 * kFewWarps, 1) few_token_ragged_kernel(const __grid_constant__ FewTokenParams p) {
+  constexpr int kRows = 8, kSlot = (TWO ? 16 : 8) * kRows;   // sums [token][row]
+  extern __shared__ __align__(16) uint8_t few_smem[];
+  float* const sums = reinterpret_cast<float*>(few_smem);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
+  const int quads = (int)((p.K + kFewCols - 1) / kFewCols);
+  const FewShare share = few_share(sums, (int)(p.N / kRows), quads, kSlot);
+  const float mean = p.scale_fp32 ? 0.0f : __ldg(p.mean);
+  const uint16_t* x0 = p.x + (int64_t)min(g, p.M - 1) * p.K;       // rows past M repeat the last one, unread
+  const uint16_t* x1 = p.x + (int64_t)min(g + 8, p.M - 1) * p.K;
+  const uint32_t lane_addr = few_fill_table(p, few_smem + (kFewTableAddr - smem_u32(few_smem)), sums);
+
+  for (int t0 = share.begin; t0 < share.end; t0 += share.per_round) {
+    const int nt = min(share.end - t0, share.per_round);
+    const int items = nt * quads;
+    const int i0 = items * warp / kFewWarps, i1 = items * (warp + 1) / kFewWarps;
+    int quad = i0 / nt, tile = i0 - quad * nt;
+    // the item fetched next: the flat index of the lane's first weight and its 8-code words before K
+    // (columns past K, where x is zero, take the last word before them)
+    int f_quad = quad, f_tile = tile, f_valid = 0;
+    int64_t f_at = 0;
+    auto place = [&]() {
+      int64_t col = (int64_t)f_quad * kFewCols + 64 * c;
+      f_valid = col >= p.K ? 1 : (int)min((p.K - col) >> 3, (int64_t)8);
+      if (col >= p.K) col = p.K - 8;
+      f_at = ((int64_t)(t0 + f_tile) * kRows + g) * p.K + col;
+    };
+    FewUnit u;
+    auto fetch = [&]() {
+      const uint32_t blk = (uint32_t)(f_at >> 6);
+      u.split = (int)((64 - (f_at & 63)) >> 3);
+      u.s0 = few_scale(p, blk);
+      u.s1 = few_scale(p, u.split < f_valid ? blk + 1 : blk);   // the next block exists where a valid word lies in it
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(p.codes + (f_at >> 1));
+#pragma unroll
+      for (int j = 0; j < 8; ++j) u.w[j] = __ldg(src + (j < f_valid ? j : 0));
+      f_at += kRows * p.K;
+      if (++f_tile == nt) {
+        f_tile = 0;
+        ++f_quad;
+        place();
+      }
+    };
+    if (i0 < i1) {
+      place();
+      fetch();
+    }
     for (int i = i0; i < i1; ++quad, tile = 0) {
       // this warp's tiles of one quad of columns: x stays in registers
       uint4 xa[8], xb[TWO ? 8 : 1];
-      const int64_t kcol = (int64_t)quad * kFewCols + 64 * c;
+      const int64_t col = (int64_t)quad * kFewCols + 64 * c;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         xa[j] = make_uint4(0u, 0u, 0u, 0u);
         if constexpr (TWO) xb[j] = xa[j];
-        if (kcol + 8 * j < p.K) {
-          xa[j] = __ldg(reinterpret_cast<const uint4*>(x0 + kcol + 8 * j));
-          if constexpr (TWO) xb[j] = __ldg(reinterpret_cast<const uint4*>(x1 + kcol + 8 * j));
+        if (col + 8 * j < p.K) {
+          xa[j] = __ldg(reinterpret_cast<const uint4*>(x0 + col + 8 * j));
+          if constexpr (TWO) xb[j] = __ldg(reinterpret_cast<const uint4*>(x1 + col + 8 * j));
         }
       }
       const int stop = min(i1, i + nt - tile);
-      float* out = sums + (tile * quads + quad) * kSlot + g * kFewRows + 2 * c;
-#pragma unroll 2
+      float* out = sums + (tile * quads + quad) * kSlot + g * kRows + 2 * c;
       for (; i < stop; ++i, out += quads * kSlot) {
-        const FewUnit<GENERIC> v = u0;
-        u0 = u1;
-        if (i + 2 < i1) fetch(u1);
-        const float s0 = p.scale_fp32 ? v.s0.value : dq_block_scale(v.s0.code, v.s0.value, mean);
-        const float s1 = !GENERIC ? s0 : p.scale_fp32 ? v.s1.value : dq_block_scale(v.s1.code, v.s1.value, mean);
-        float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        const FewUnit v = u;
+        if (i + 1 < i1) fetch();
+        const float s0 = few_scale_value(p, v.s0, mean), s1 = few_scale_value(p, v.s1, mean);
+        float acc0[4] = {0.0f, 0.0f, 0.0f, 0.0f}, acc1[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float sc = (GENERIC && j >= v.split) ? s1 : s0;
           uint32_t b[4];
-#pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            const uint32_t at = prmt(v.w[j], lane_addr, 0x7604u | ((uint32_t)h << 4));
-            uint64_t q;
-            asm("ld.shared.b64 %0, [%1];" : "=l"(q) : "r"(at));   // the table does not change any more
-            q = f32x2_mul(q, f32_pair(sc, sc));
-            b[h] = pack_bf16x2(pair_lo(q), pair_hi(q));
+          few_expand8(v.w[j], j >= v.split ? s1 : s0, lane_addr, b);
+          if constexpr (TWO) {
+            mma_bf16_16816(acc0, xa[j].x, xb[j].x, xa[j].y, xb[j].y, b[0], b[1]);
+            mma_bf16_16816(acc1, xa[j].z, xb[j].z, xa[j].w, xb[j].w, b[2], b[3]);
+          } else {
+            // The four x registers as they were loaded are the A operand of both products (any other
+            // order would have to be moved together each time).  Rows 0-7 then hold columns 0, 1, 4, 5
+            // of the 8 and rows 8-15 columns 2, 3, 6, 7: with the weights of the former the upper
+            // half of the sums is the tokens', with those of the latter the lower half.
+            mma_bf16_16816(acc0, xa[j].x, xa[j].y, xa[j].z, xa[j].w, b[0], b[2]);
+            mma_bf16_16816(acc1, xa[j].x, xa[j].y, xa[j].z, xa[j].w, b[1], b[3]);
           }
-          const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-          const uint4& y = TWO ? xb[j] : zero;
-          mma_bf16_16816(acc, xa[j].x, y.x, xa[j].y, y.y, b[0], b[1]);
-          mma_bf16_16816(acc, xa[j].z, y.z, xa[j].w, y.w, b[2], b[3]);
         }
-        // accumulators: token g (and g + 8), rows 2 c and 2 c + 1
-        *reinterpret_cast<float2*>(out) = make_float2(acc[0], acc[1]);
-        if constexpr (TWO) *reinterpret_cast<float2*>(out + 8 * kFewRows) = make_float2(acc[2], acc[3]);
+        // sums of token g (and g + 8), rows 2 c and 2 c + 1
+        if constexpr (TWO) {
+          *reinterpret_cast<float2*>(out) = make_float2(acc0[0] + acc1[0], acc0[1] + acc1[1]);
+          *reinterpret_cast<float2*>(out + 8 * kRows) = make_float2(acc0[2] + acc1[2], acc0[3] + acc1[3]);
+        } else {
+          *reinterpret_cast<float2*>(out) = make_float2(acc0[0] + acc1[2], acc0[1] + acc1[3]);
+        }
       }
     }
     if (p.t) {
@@ -281,7 +520,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) few_token_kernel(const __gr
       const float* ta = p.t + (int64_t)min(g, p.M - 1) * p.r;
       const float* tb = p.t + (int64_t)min(g + 8, p.M - 1) * p.r;
       for (int tl = warp; tl < nt; tl += kFewWarps) {
-        const uint16_t* brow = p.B + ((t0 + tl) * kFewRows + g) * p.r;
+        const uint16_t* brow = p.B + ((int64_t)(t0 + tl) * kRows + g) * p.r;
         float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         for (int j = 4 * c; j < p.r + 4 * c; j += 16) {   // 16 rank columns a step: lane c takes 4 of them
           float4 va = make_float4(0.0f, 0.0f, 0.0f, 0.0f), vb = va;
@@ -299,65 +538,53 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) few_token_kernel(const __gr
           mma_bf16_16816(acc, ha0, hb0, ha1, hb1, bv.x, bv.y);
           mma_bf16_16816(acc, la0, lb0, la1, lb1, bv.x, bv.y);
         }
-        float* out = sums + (nt * quads + tl) * kSlot + g * kFewRows + 2 * c;
+        float* out = sums + (nt * quads + tl) * kSlot + g * kRows + 2 * c;
         *reinterpret_cast<float2*>(out) = make_float2(acc[0], acc[1]);
-        if constexpr (TWO) *reinterpret_cast<float2*>(out + 8 * kFewRows) = make_float2(acc[2], acc[3]);
+        if constexpr (TWO) *reinterpret_cast<float2*>(out + 8 * kRows) = make_float2(acc[2], acc[3]);
       }
     }
     __syncthreads();
-    for (int o = threadIdx.x; o < nt * kFewRows * p.M; o += 32 * kFewWarps) {
-      const int row = o % kFewRows, rest = o / kFewRows, tl = rest % nt, tok = rest / nt;
-      const int64_t n = (t0 + tl) * kFewRows + row;
-      float z = 0.0f;
-      const float* part = sums + tl * quads * kSlot + tok * kFewRows + row;
-#pragma unroll 8
-      for (int w = 0; w < quads; ++w) z += part[w * kSlot];
-      if (p.t) z += sums[(nt * quads + tl) * kSlot + tok * kFewRows + row];
-      if (p.post.bias) z += __uint_as_float((uint32_t)p.post.bias[n] << 16);
-      const int64_t at = (int64_t)tok * p.N + n;
-      if (p.post.z) p.post.z[at] = __bfloat16_as_ushort(__float2bfloat16_rn(z));
-      float v[2] = {z, 0.0f};
-      act_apply(v, p.post.act);
-      if (p.post.residual) v[0] += __uint_as_float((uint32_t)p.post.residual[at] << 16);
-      p.y[at] = __bfloat16_as_ushort(__float2bfloat16_rn(v[0]));
-    }
+    few_finish<kRows>(p, sums, kSlot, t0, nt, quads, [](int row, int tok) { return tok * kRows + row; });
     __syncthreads();   // the sums are free for the next round
   }
 }
 
-// Whether this path takes the shape: few tokens, a row's items fit the sums, block numbers 32 bits.
-// Nine to sixteen tokens double the registers of x and the sums of an item, and with long rows the
-// fused GEMM's 16-token tiles are then faster: at 16 tokens 72 against 58 us for 5120 x 13824, but 53
-// against 55 us for 13824 x 5120, 27 against 34 us for 5120 x 5120 and 19 against 27 us for 4096 x
-// 4096.  Up to 8 tokens this path takes 0.35 to 0.6 of the tiles' time.
+// Whether this path takes the shape: few tokens, a row's items fit the sums (16 rows x 8 or 16 tokens
+// each), block numbers 32 bits.
 static bool few_token_fits(int64_t M, int64_t K, int64_t N) {
-  if (M > 8 && K > 8192) return false;
-  return M <= kFewTokens && (K + kFewCols - 1) / kFewCols < few_slots(M > 8) && N * K < (1ll << 37);
+  if (M > kFewTokens || N * K >= (1ll << 37)) return false;
+  const int64_t quads = (K + kFewCols - 1) / kFewCols;
+  return quads + 1 <= kFewSumBytes / (4 * 16 * (M > 8 ? 16 : 8));
 }
 
-template <bool TWO, bool GENERIC>
-static cudaError_t launch_few_token_t(const FewTokenParams& p, cudaStream_t st) {
-  static std::atomic<uint64_t> configured{0};
-  cudaError_t e = enable_smem_once(few_token_kernel<TWO, GENERIC>, kFewSmemBytes, configured);
+static cudaError_t launch_few_token_k(void (*kernel)(const FewTokenParams), std::atomic<uint64_t>& configured, int smem,
+                                      int64_t tiles, const FewTokenParams& p, cudaStream_t st) {
+  cudaError_t e = enable_smem_once(kernel, smem, configured);
   if (e != cudaSuccess) return e;
   int dev = 0, sms = 148;
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)std::min<int64_t>(sms, p.N / kFewRows));
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>(sms, tiles));
   cfg.blockDim = dim3(32 * kFewWarps);
-  cfg.dynamicSmemBytes = kFewSmemBytes;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = p.t ? 1 : 0;   // with adapters the grid before is the one that makes t
-  return cudaLaunchKernelEx(&cfg, few_token_kernel<TWO, GENERIC>, p);
+  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 static cudaError_t launch_few_token(const FewTokenParams& p, cudaStream_t st) {
-  if (p.M <= 8) return p.K % 64 ? launch_few_token_t<false, true>(p, st) : launch_few_token_t<false, false>(p, st);
-  return p.K % 64 ? launch_few_token_t<true, true>(p, st) : launch_few_token_t<true, false>(p, st);
+  static std::atomic<uint64_t> configured[4] = {{0}, {0}, {0}, {0}};
+  if (p.K % 64 == 0) {
+    const int64_t tiles = (p.N + 15) / 16;
+    return p.M <= 8 ? launch_few_token_k(few_token_kernel<false>, configured[0], kFewSmemBytes, tiles, p, st)
+                    : launch_few_token_k(few_token_kernel<true>, configured[1], kFewSmemBytes, tiles, p, st);
+  }
+  return p.M <= 8 ? launch_few_token_k(few_token_ragged_kernel<false>, configured[2], kFewRaggedSmemBytes, p.N / 8, p, st)
+                  : launch_few_token_k(few_token_ragged_kernel<true>, configured[3], kFewRaggedSmemBytes, p.N / 8, p, st);
 }
 
 static cudaError_t launch_few_token_down(const FewTokenDownParams& p, cudaStream_t st) {

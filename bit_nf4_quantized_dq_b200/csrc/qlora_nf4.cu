@@ -81,9 +81,10 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// 2-D map over a row-major [outer][inner] array with row pitch `row_bytes`.
+// 2-D map over a row-major [outer][inner] array with row pitch `row_bytes`; bf16 boxes land with the
+// 128-byte swizzle, byte boxes plainly unless `swizzle_bytes`.
 int make_map(CUtensorMap* m, const void* base, bool bf16, uint64_t inner, uint64_t outer, uint64_t row_bytes,
-             uint32_t box_inner, uint32_t box_outer) {
+             uint32_t box_inner, uint32_t box_outer, bool swizzle_bytes = false) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return fail(QNF4_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
   if (!aligned(base, 16) || row_bytes % 16 != 0)
@@ -95,7 +96,7 @@ int make_map(CUtensorMap* m, const void* base, bool bf16, uint64_t inner, uint64
   cuuint32_t estr[2] = {1, 1};
   CUresult r = enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
                    const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   bf16 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                   bf16 || swizzle_bytes ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(QNF4_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
   return QNF4_OK;
@@ -772,8 +773,25 @@ int linear_fwd_impl(const uint16_t* x, const LinearShape& sh, int codebook, int 
       if (e != cudaSuccess) return cuda_fail(e, "few-token down-projection launch");
     }
     mark(1, st);
-    const qnf4::FewTokenParams fp{x,  (int32_t)M, K, N, codes, scale_codes, c2, mean, double_quant ? 0 : 1,
-                                  cb, t,          B, r, *post, y};
+    qnf4::FewTokenParams fp;
+    memset(&fp, 0, sizeof(fp));
+    if (K % 64 == 0)
+      if (int rc = make_map(&fp.map, codes, false, K / 2, N, K / 2, qnf4::kFewCols / 2, 16, true)) return rc;
+    fp.x = x;
+    fp.M = (int32_t)M;
+    fp.K = K;
+    fp.N = N;
+    fp.codes = codes;
+    fp.scale_codes = scale_codes;
+    fp.scales = c2;
+    fp.mean = mean;
+    fp.scale_fp32 = double_quant ? 0 : 1;
+    fp.cb = cb;
+    fp.t = t;
+    fp.B = B;
+    fp.r = r;
+    fp.post = *post;
+    fp.y = y;
     cudaError_t e = qnf4::launch_few_token(fp, st);
     if (e != cudaSuccess) return cuda_fail(e, "few-token launch");
     mark(2, st);
