@@ -21,7 +21,7 @@
 //    more than an empty loop, at 36 MB.)  The 128-byte swizzle lets the lanes read them without bank
 //    conflicts.  The scales are one item ahead in registers.
 //  - tcgen05 would need the tile staged for 128 rows and at least 16 tokens; as 16-token tiles of the
-//    fused GEMM (with its K splits and a reduction) the same layer takes 52 us.
+//    fused GEMM (with its K splits and a reduction) the same layer takes 52 us, here 22 us.
 // With K % 64 != 0 code rows are only 4-byte aligned and blocks span rows: a kernel of its own reads
 // the codes into registers, in tiles of 8 rows.
 #pragma once
@@ -46,8 +46,9 @@ constexpr int kFewRingBytes = kFewWarps * kFewRing * kFewItemBytes;
 constexpr int kFewSmemBytes = (int)kFewRingAddr + kFewRingBytes + kFewWarps * kFewRing * 8 + 16;
 static_assert(kFewSmemBytes <= 227 * 1024, "shared memory of one block");
 constexpr int kFewRaggedSmemBytes = (int)kFewRingAddr;
-// Bytes of sums that every launch has room for (the block's part starts at most 2 KB up).
-constexpr int kFewSumBytes = 62 * 1024;
+// Room for sums: the block's part of shared memory starts 1 KB up.  (The kernels measure it, and take
+// their tiles in more rounds if there is less.)
+constexpr int kFewSumBytes = 63 * 1024;
 
 struct FewTokenParams {
   CUtensorMap map;         // codes [N][K / 2], boxes of 16 rows x 128 bytes, 128-byte swizzle (K % 64 == 0)
@@ -65,6 +66,7 @@ struct FewTokenParams {
   int32_t r;
   EpiArgs post;
   uint16_t* y;             // [M][N]
+  float* part;             // [quads of columns + 1][M][N] sums of the items (flat list), or NULL
 };
 
 // t[m][j] = s sum_k x[m][k] A[j][k]: one block per rank column and kFewDownTokens tokens.
@@ -215,7 +217,9 @@ __device__ __forceinline__ void few_finish(const FewTokenParams& p, const float*
 }
 
 // K % 64 == 0.  TWO: more than 8 tokens.
-template <bool TWO>
+// FLAT: the blocks share one list of all items, columns outermost, whatever tile they cut; every item
+// leaves its sums in p.part for few_token_join_kernel.
+template <bool TWO, bool FLAT>
 __global__ void __launch_bounds__(32 * kFewWarps, 1) few_token_kernel(const __grid_constant__ FewTokenParams p) {
   constexpr int kRows = 16, NT = TWO ? 2 : 1, kSlot = NT * kRows * 8;   // sums [group of 8 tokens][row][token]
   extern __shared__ __align__(16) uint8_t few_smem[];
@@ -235,16 +239,31 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) few_token_kernel(const __gr
   __syncthreads();
 
   const int quads = (int)((p.K + kFewCols - 1) / kFewCols);
-  const FewShare share = few_share(sums, (int)((p.N + kRows - 1) / kRows), quads, kSlot);
+  const int tiles = (int)((p.N + kRows - 1) / kRows);
+  const FewShare share = FLAT ? FewShare{0, tiles, tiles} : few_share(sums, tiles, quads, kSlot);
   const float mean = p.scale_fp32 ? 0.0f : __ldg(p.mean);
   uint32_t lane_addr = 0u;
   int slot = 0, pending = 0;     // the ring's slot read next, and its loads on their way
   uint32_t phase = 0u;
   bool ok = true;
+  // FLAT: an item's sums of rows g and g + 8, tokens 2 c and 2 c + 1 of group t
+  auto store_flat = [&](int at_quad, int at_tile, int t, const float (&v)[4]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int tok = 8 * t + 2 * c + (k & 1);
+      const int64_t n = (int64_t)at_tile * kRows + g + 8 * (k >> 1);
+      if (tok < p.M && n < p.N) p.part[((int64_t)at_quad * p.M + tok) * p.N + n] = v[k];
+    }
+  };
   for (int t0 = share.begin; t0 < share.end; t0 += share.per_round) {
     const int nt = min(share.end - t0, share.per_round);
     const int items = nt * quads;
-    const int i0 = items * warp / kFewWarps, i1 = items * (warp + 1) / kFewWarps;
+    int i0 = items * warp / kFewWarps, i1 = items * (warp + 1) / kFewWarps;
+    if constexpr (FLAT) {
+      const int64_t parts = (int64_t)gridDim.x * kFewWarps, part = (int64_t)blockIdx.x * kFewWarps + warp;
+      i0 = (int)(items * part / parts);
+      i1 = (int)(items * (part + 1) / parts);
+    }
     int quad = i0 / nt, tile = i0 - quad * nt;
     // the item whose codes are loaded next
     int c_quad = quad, c_tile = tile, c_left = i1 - i0;
@@ -353,10 +372,18 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) few_token_kernel(const __gr
         // sums of rows g and g + 8, tokens 2 c and 2 c + 1 of each group
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          *reinterpret_cast<float2*>(out + t * 128) = make_float2(acc[t][0][0] + acc[t][1][0], acc[t][0][1] + acc[t][1][1]);
-          *reinterpret_cast<float2*>(out + t * 128 + 64) =
-              make_float2(acc[t][0][2] + acc[t][1][2], acc[t][0][3] + acc[t][1][3]);
+          if constexpr (FLAT) {
+            const float both[4] = {acc[t][0][0] + acc[t][1][0], acc[t][0][1] + acc[t][1][1],
+                                   acc[t][0][2] + acc[t][1][2], acc[t][0][3] + acc[t][1][3]};
+            store_flat(quad, tile, t, both);
+          } else {
+            *reinterpret_cast<float2*>(out + t * 128) =
+                make_float2(acc[t][0][0] + acc[t][1][0], acc[t][0][1] + acc[t][1][1]);
+            *reinterpret_cast<float2*>(out + t * 128 + 64) =
+                make_float2(acc[t][0][2] + acc[t][1][2], acc[t][0][3] + acc[t][1][3]);
+          }
         }
+        if constexpr (FLAT) ++tile;
       }
       ++quad;
       tile = 0;
@@ -365,7 +392,8 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) few_token_kernel(const __gr
     if (p.t) {
       // t B^T: t as bf16 hi + lo (16 significant bits), one more slot of sums per tile
       asm volatile("griddepcontrol.wait;" ::: "memory");   // t comes from the grid before
-      for (int tl = warp; tl < nt; tl += kFewWarps) {
+      const int first = FLAT ? (int)blockIdx.x * kFewWarps + warp : warp, step = FLAT ? (int)gridDim.x * kFewWarps : kFewWarps;
+      for (int tl = first; tl < nt; tl += step) {
         const int64_t n0 = (int64_t)(t0 + tl) * kRows + g, n1 = min(n0 + 8, p.N - 1);
         float acc[NT][4];
 #pragma unroll
@@ -392,13 +420,17 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) few_token_kernel(const __gr
         float* out = sums + (nt * quads + tl) * kSlot + g * 8 + 2 * c;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          *reinterpret_cast<float2*>(out + t * 128) = make_float2(acc[t][0], acc[t][1]);
-          *reinterpret_cast<float2*>(out + t * 128 + 64) = make_float2(acc[t][2], acc[t][3]);
+          if constexpr (FLAT) {
+            store_flat(quads, tl, t, acc[t]);
+          } else {
+            *reinterpret_cast<float2*>(out + t * 128) = make_float2(acc[t][0], acc[t][1]);
+            *reinterpret_cast<float2*>(out + t * 128 + 64) = make_float2(acc[t][2], acc[t][3]);
+          }
         }
       }
     }
     __syncthreads();
-    if (*abort_word) break;   // the same for every thread: all waits of the round are over
+    if (FLAT || *abort_word) break;   // the same for every thread: all waits of the round are over
     few_finish<kRows>(p, sums, kSlot, t0, nt, quads, [](int row, int tok) { return (tok >> 3) * 128 + row * 8 + (tok & 7); });
     __syncthreads();          // the sums are free for the next round
   }
@@ -410,6 +442,38 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) few_token_kernel(const __gr
       for (int i = 0; i < (1 << 20) && !mbar_try_wait(&full[s], ph); ++i) {}
     }
   }
+}
+
+// Joins a flat list's `parts` sums per output (the quads of columns and, behind them, the adapter term):
+// y of 32 features of one token per block.  Warp w adds the parts w, w + 8, ...; the warps' sums are
+// added in their order.
+__global__ void __launch_bounds__(256) few_token_join_kernel(const __grid_constant__ FewTokenParams p, int parts) {
+  __shared__ float sums[8][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tok = blockIdx.y;
+  const int64_t n = (int64_t)blockIdx.x * 32 + lane;
+  float v = 0.0f, bias = 0.0f, res = 0.0f;
+  const int64_t to = (int64_t)tok * p.N + n;
+  if (n < p.N) {   // inputs of the call, not of the grid before
+    if (p.post.bias) bias = __uint_as_float((uint32_t)p.post.bias[n] << 16);
+    if (p.post.residual) res = __uint_as_float((uint32_t)p.post.residual[to] << 16);
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (n < p.N) {
+    const float* part = p.part + to;
+#pragma unroll 8
+    for (int w = warp; w < parts; w += 8) v += part[(int64_t)w * p.M * p.N];
+  }
+  sums[warp][lane] = v;
+  __syncthreads();
+  if (warp != 0 || n >= p.N) return;
+  float z = 0.0f;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) z += sums[w][lane];
+  z += bias;
+  if (p.post.z) p.post.z[to] = __bfloat16_as_ushort(__float2bfloat16_rn(z));
+  float a[2] = {z, 0.0f};
+  act_apply(a, p.post.act);
+  p.y[to] = __bfloat16_as_ushort(__float2bfloat16_rn(p.post.residual ? a[0] + res : a[0]));
 }
 
 // K % 64 != 0: what a lane holds of its row's 64 columns in the next item.
@@ -549,22 +613,30 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) few_token_ragged_kernel(con
   }
 }
 
-// Whether this path takes the shape: few tokens, a row's items fit the sums (16 rows x 8 or 16 tokens
-// each), block numbers 32 bits.
-static bool few_token_fits(int64_t M, int64_t K, int64_t N) {
-  if (M > kFewTokens || N * K >= (1ll << 37)) return false;
-  const int64_t quads = (K + kFewCols - 1) / kFewCols;
-  return quads + 1 <= kFewSumBytes / (4 * 16 * (M > 8 ? 16 : 8));
+// How this path takes a shape.  Whole tiles join their sums in the block that owns them, where all of
+// a block's sums fit and the tiles load the SMs evenly.  Otherwise a flat list of the items over all
+// blocks loads them evenly and a second kernel joins, about 1 us more: with adapters and one token 22.8
+// against 22.2 us for 13824 x 5120 and 12.2 against 11.3 us for 4096 x 4096, but 25 against 33 us for
+// 5120 x 13824 (two or three tiles of 54 items per SM), and 42 against 51 us for 16 tokens of 13824 x
+// 5120, whose sums would take two rounds.
+enum FewPlan : int { kFewNo = 0, kFewTiles = 1, kFewFlat = 2 };
+static FewPlan few_token_plan(int64_t M, int64_t K, int64_t N) {
+  if (M > kFewTokens || N * K >= (1ll << 37)) return kFewNo;
+  const int64_t quads = (K + kFewCols - 1) / kFewCols, tokens = M > 8 ? 16 : 8;
+  if (K % 64) return (quads + 1) * tokens * 8 * 4 <= kFewSumBytes ? kFewTiles : kFewNo;
+  const int64_t tiles = (N + 15) / 16, most = (tiles + 147) / 148;   // tiles of the fullest SM
+  const bool fits = most * (quads + 1) * tokens * 16 * 4 <= kFewSumBytes;
+  return fits && most * quads - tiles * quads / 148 <= 12 ? kFewTiles : kFewFlat;
 }
 
 static cudaError_t launch_few_token_k(void (*kernel)(const FewTokenParams), std::atomic<uint64_t>& configured, int smem,
-                                      int64_t tiles, const FewTokenParams& p, cudaStream_t st) {
+                                      int64_t blocks, const FewTokenParams& p, cudaStream_t st) {
   cudaError_t e = enable_smem_once(kernel, smem, configured);
   if (e != cudaSuccess) return e;
   int dev = 0, sms = 148;
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)std::min<int64_t>(sms, tiles));
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>(sms, blocks));
   cfg.blockDim = dim3(32 * kFewWarps);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -576,15 +648,29 @@ static cudaError_t launch_few_token_k(void (*kernel)(const FewTokenParams), std:
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-static cudaError_t launch_few_token(const FewTokenParams& p, cudaStream_t st) {
-  static std::atomic<uint64_t> configured[4] = {{0}, {0}, {0}, {0}};
-  if (p.K % 64 == 0) {
-    const int64_t tiles = (p.N + 15) / 16;
-    return p.M <= 8 ? launch_few_token_k(few_token_kernel<false>, configured[0], kFewSmemBytes, tiles, p, st)
-                    : launch_few_token_k(few_token_kernel<true>, configured[1], kFewSmemBytes, tiles, p, st);
-  }
-  return p.M <= 8 ? launch_few_token_k(few_token_ragged_kernel<false>, configured[2], kFewRaggedSmemBytes, p.N / 8, p, st)
-                  : launch_few_token_k(few_token_ragged_kernel<true>, configured[3], kFewRaggedSmemBytes, p.N / 8, p, st);
+static cudaError_t launch_few_token(const FewTokenParams& p, FewPlan plan, cudaStream_t st) {
+  static std::atomic<uint64_t> configured[6] = {{0}, {0}, {0}, {0}, {0}, {0}};
+  const int64_t tiles = (p.N + 15) / 16, quads = (p.K + kFewCols - 1) / kFewCols;
+  if (p.K % 64)
+    return p.M <= 8 ? launch_few_token_k(few_token_ragged_kernel<false>, configured[0], kFewRaggedSmemBytes, p.N / 8, p, st)
+                    : launch_few_token_k(few_token_ragged_kernel<true>, configured[1], kFewRaggedSmemBytes, p.N / 8, p, st);
+  if (plan == kFewTiles)
+    return p.M <= 8 ? launch_few_token_k(few_token_kernel<false, false>, configured[2], kFewSmemBytes, tiles, p, st)
+                    : launch_few_token_k(few_token_kernel<true, false>, configured[3], kFewSmemBytes, tiles, p, st);
+  cudaError_t e = p.M <= 8
+                      ? launch_few_token_k(few_token_kernel<false, true>, configured[4], kFewSmemBytes, tiles * quads, p, st)
+                      : launch_few_token_k(few_token_kernel<true, true>, configured[5], kFewSmemBytes, tiles * quads, p, st);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((p.N + 31) / 32), (unsigned)p.M);
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, few_token_join_kernel, p, (int)quads + (p.t ? 1 : 0));
 }
 
 static cudaError_t launch_few_token_down(const FewTokenDownParams& p, cudaStream_t st) {

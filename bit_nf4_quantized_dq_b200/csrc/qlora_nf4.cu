@@ -235,6 +235,19 @@ size_t fwd_carve(Carver& c, const LinearShape& s, const FwdPlan& p, FwdWs* w) {
   return c.off;
 }
 
+// The few-token path: t and, for a flat list of items, their sums.
+struct FewWs {
+  float *t, *part;
+};
+
+size_t few_carve(Carver& c, const LinearShape& s, qnf4::FewPlan plan, FewWs* w) {
+  w->t = c.take<float>((size_t)s.M * s.r);
+  w->part = plan == qnf4::kFewFlat
+                ? c.take<float>((size_t)((s.K + qnf4::kFewCols - 1) / qnf4::kFewCols + 1) * s.M * s.N)
+                : nullptr;
+  return c.off;
+}
+
 struct BwdWs {
   uint16_t *Bt, *uhi, *ulo, *uT3, *tT3;
   double* partial;
@@ -758,16 +771,17 @@ int linear_fwd_impl(const uint16_t* x, const LinearShape& sh, int codebook, int 
   if (!aligned(x, 16) || !aligned(A, 16) || !aligned(B, 16) || !aligned(y, 16) || !aligned(codes, 16) ||
       !aligned(t_saved, 16) || !aligned(workspace, 256))
     return fail(QNF4_ERR_UNSUPPORTED, "alignment: operands 16 B, workspace 256 B");
+  const qnf4::FewPlan few = post ? qnf4::few_token_plan(M, K, N) : qnf4::kFewNo;
   const FwdPlan plan = plan_fwd(sh);
   Carver c{static_cast<char*>(workspace)};
   FwdWs w;
-  const size_t need = fwd_carve(c, sh, plan, &w);
+  FewWs fw;
+  const size_t need = few != qnf4::kFewNo ? few_carve(c, sh, few, &fw) : fwd_carve(c, sh, plan, &w);
   if (workspace_bytes < need) return fail(QNF4_ERR_WORKSPACE, "workspace needs %zu bytes", need);
   if (int rc = check_arch()) return rc;
   mark(0, st);
-  if (post && qnf4::few_token_fits(M, K, N)) {
-    // the workspace of the tile path holds t (M r floats) with room to spare
-    float* t = A ? (t_saved ? t_saved : static_cast<float*>(workspace)) : nullptr;
+  if (few != qnf4::kFewNo) {
+    float* t = A ? (t_saved ? t_saved : fw.t) : nullptr;
     if (A) {
       cudaError_t e = qnf4::launch_few_token_down(qnf4::FewTokenDownParams{x, A, (int32_t)M, r, K, s, t}, st);
       if (e != cudaSuccess) return cuda_fail(e, "few-token down-projection launch");
@@ -792,7 +806,8 @@ int linear_fwd_impl(const uint16_t* x, const LinearShape& sh, int codebook, int 
     fp.r = r;
     fp.post = *post;
     fp.y = y;
-    cudaError_t e = qnf4::launch_few_token(fp, st);
+    fp.part = fw.part;
+    cudaError_t e = qnf4::launch_few_token(fp, few, st);
     if (e != cudaSuccess) return cuda_fail(e, "few-token launch");
     mark(2, st);
     return QNF4_OK;
@@ -1089,7 +1104,9 @@ size_t qlora_linear_epi_fwd_workspace_bytes(int64_t M, int64_t K, int64_t N, int
   LinearShape s{M, K, N, r};
   Carver c{nullptr};
   FwdWs w;
-  return std::max<size_t>(fwd_carve(c, s, plan_fwd(s), &w), 256);
+  FewWs fw;
+  const qnf4::FewPlan few = qnf4::few_token_plan(M, K, N);
+  return std::max<size_t>(few != qnf4::kFewNo ? few_carve(c, s, few, &fw) : fwd_carve(c, s, plan_fwd(s), &w), 256);
 }
 
 size_t qlora_epilogue_bwd_workspace_bytes(int64_t M, int64_t N) {

@@ -283,6 +283,31 @@ def test_linear_epilogue_other_formats(codebook, dq):
         assert_within_tolerance(y, _epi_ref(inp["x"], Wd, inp["A"], inp["B"], 0.5, bias, "silu", res)[0], f"{M}")
 
 
+@pytest.mark.parametrize("M,N,K,r", [(1, 5120, 4096, 16), (3, 2376, 3968, 8), (8, 40, 13824, 24), (9, 2376, 3968, 64),
+                                     (16, 1000, 20480, 8), (16, 2376, 256, 16), (11, 24, 33024, 0), (2, 1208, 64, 8),
+                                     (5, 2376, 2056, 8), (13, 8, 2056, 16)])
+def test_few_tokens_joined_in_a_block_and_from_a_flat_list(M, N, K, r):
+    """Shapes on both sides of the few-token path's rule: tiles of one block, several rounds of them, a
+    flat list whose items cut tiles, a last tile of 8 rows, rows longer than the sums of a block hold,
+    rows that are no multiple of 64; sampled outputs against the oracle."""
+    W = _weight(N, K, 111)
+    Wq = q.nf4_quantize_dq(W.cuda())
+    Wd = to_np64(q.nf4_dequant(Wq))              # bit-exact against the oracle elsewhere
+    inp = synth.linear_inputs(M, N, K, max(r, 8), 112)
+    A, B = (inp["A"], inp["B"]) if r else (None, None)
+    x = (inp["x"].float() / 16).to(BF)
+    bias, res = _normal((N,), 0.5, 113), _normal((M, N), 2.0, 114)
+    y, t, z = q.qlora_linear_epilogue_fwd(x.cuda(), Wq, _c(A), _c(B), 0.5, bias=bias.cuda(), activation="silu",
+                                          residual=res.cuda(), save=True)
+    again = q.qlora_linear_epilogue_fwd(x.cuda(), Wq, _c(A), _c(B), 0.5, bias=bias.cuda(), activation="silu",
+                                        residual=res.cuda())
+    torch.cuda.synchronize()
+    assert q.check_device_error() == 0 and torch.equal(again[0], y)
+    yr, zr, _ = _epi_ref(x, Wd, A, B, 0.5, bias, "silu", res)
+    assert_within_tolerance(y, yr, "y")
+    assert_within_tolerance(z, zr, "z")
+
+
 def test_linear_epilogue_identity_reproduces_the_weight():
     """x = I without anything behind the product: y = W'^T bit for bit, through the few-token path too."""
     for N, K in ((384, 256), (200, 1000)):
