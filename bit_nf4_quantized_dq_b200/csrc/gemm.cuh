@@ -890,10 +890,10 @@ cudaError_t launch_gemm(const GemmParams& p, int bn, cudaStream_t st) {
 // small helpers of the low-rank path
 // ---------------------------------------------------------------------------------------
 // out[c][r] = in[r][c] (bf16), 32x32 tiles through shared memory.
-__global__ void transpose_bf16_kernel(const uint16_t* __restrict__ in, int64_t rows, int64_t cols,
-                                      uint16_t* __restrict__ out, int64_t ld_out) {
+// one 32 x 32 tile by 32 x 8 threads
+__device__ __forceinline__ void transpose_bf16_tile(const uint16_t* __restrict__ in, int64_t rows, int64_t cols,
+                                                    uint16_t* __restrict__ out, int64_t ld_out, int64_t r0, int64_t c0) {
   __shared__ uint16_t tile[32][33];
-  const int64_t r0 = (int64_t)blockIdx.y * 32, c0 = (int64_t)blockIdx.x * 32;
   for (int i = threadIdx.y; i < 32; i += blockDim.y) {
     const int64_t r = r0 + i, c = c0 + threadIdx.x;
     if (r < rows && c < cols) tile[i][threadIdx.x] = in[r * cols + c];
@@ -903,6 +903,11 @@ __global__ void transpose_bf16_kernel(const uint16_t* __restrict__ in, int64_t r
     const int64_t c = c0 + i, r = r0 + threadIdx.x;
     if (r < rows && c < cols) out[c * ld_out + r] = tile[threadIdx.x][i];
   }
+}
+
+__global__ void transpose_bf16_kernel(const uint16_t* __restrict__ in, int64_t rows, int64_t cols,
+                                      uint16_t* __restrict__ out, int64_t ld_out) {
+  transpose_bf16_tile(in, rows, cols, out, ld_out, (int64_t)blockIdx.y * 32, (int64_t)blockIdx.x * 32);
 }
 
 

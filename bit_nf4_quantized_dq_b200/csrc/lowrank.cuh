@@ -26,6 +26,7 @@
 #pragma once
 
 #include "act8.cuh"
+#include "gemm.cuh"
 #include "nf4_device.cuh"
 
 namespace qnf4 {
@@ -38,6 +39,9 @@ struct LowRankParams {
   int32_t splits, kb_per_split;
   int32_t rows, cols;     // valid extent: rows on the UMMA M side, cols = rank columns
   double* partial;        // [splits][cols][rows] float64
+  // With one split, the gradient itself instead (bf16; NULL: `partial`): [cols][rows], or [rows][cols]
+  uint16_t* grad;
+  int32_t grad_by_row;
   // A operand held as an 8-bit checkpoint (act8.cuh), MN-major: its scales [a8_tokens][a8_groups]
   const uint8_t* a8_scales;
   int32_t a8_tokens, a8_groups;
@@ -129,9 +133,13 @@ __device__ __forceinline__ void two_sum_acc(uint64_t& hi, uint64_t& lo, uint64_t
   lo = f2_add(lo, e);
 }
 
+__device__ __forceinline__ uint16_t bf16_bits_rn(double v) {
+  return __bfloat16_as_ushort(__float2bfloat16_rn((float)v));
+}
+
+// One block's part: rows 128 tile_row .., columns BJ tile_col .., the k-blocks of `split`.
 template <int BJ, int TERMS, bool A8>
-__global__ void __launch_bounds__(LrCfg<BJ, TERMS, A8>::kThreads, 1)
-    lowrank_kernel(const __grid_constant__ LowRankParams p) {
+__device__ __forceinline__ void lowrank_block(const LowRankParams& p, int tile_row, int tile_col, int split) {
   using C = LrCfg<BJ, TERMS, A8>;
   constexpr int S = C::kStages;
   extern __shared__ uint8_t smem_dyn[];
@@ -146,7 +154,7 @@ __global__ void __launch_bounds__(LrCfg<BJ, TERMS, A8>::kThreads, 1)
   uint64_t* prod = accempty + NB + 1;  // [S] with A8: the decoded A tile is in place (behind the two words above)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row0 = blockIdx.x * 128, col0 = blockIdx.y * BJ, split = blockIdx.z;
+  const int row0 = tile_row * 128, col0 = tile_col * BJ;
   const int kb_begin = split * p.kb_per_split;
   int kb_end = kb_begin + p.kb_per_split;
   if (kb_end > p.kblocks) kb_end = p.kblocks;
@@ -304,7 +312,7 @@ __global__ void __launch_bounds__(LrCfg<BJ, TERMS, A8>::kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&prod[s]);
     }
-  } else {
+  } else if (warp < kLrA8Warp0) {   // (a block of the paired launch has idle warps behind these)
     // ------------------------------------------------------------------ flush to float64
     // Group g (warps 2-5, then 7-10) drains columns [g * HALF, (g + 1) * HALF) of each
     // k-block's accumulator; warp w reads TMEM lanes 32 (w % 4) .. 32 (w % 4) + 31.  With
@@ -345,14 +353,36 @@ __global__ void __launch_bounds__(LrCfg<BJ, TERMS, A8>::kThreads, 1)
       if (lane == 0) mbar_arrive(&accempty[buf]);
     }
     if (ok && active && row < p.rows) {
-      double* out = p.partial + (int64_t)split * p.cols * p.rows;
-#pragma unroll
-      for (int j = 0; j < HALF; ++j) {
-        const int col = col0 + c0 + j;
+      auto sum = [&](int j) {   // hi + lo of column c0 + j
         const uint64_t h = hi[j / 2], l = lo[j / 2];
         const float hj = __uint_as_float((uint32_t)(j & 1 ? h >> 32 : h));
         const float lj = __uint_as_float((uint32_t)(j & 1 ? l >> 32 : l));
-        if (col < p.cols) out[(int64_t)col * p.rows + row] = (double)hj + (double)lj;
+        return (double)hj + (double)lj;
+      };
+      if (TERMS == 3 && p.grad) {
+        // as finalize_grad_tile rounds it (which adds the splits to 0.0)
+#pragma unroll
+        for (int j0 = 0; j0 < HALF; j0 += 8) {
+          const int col = col0 + c0 + j0;   // the columns are a multiple of 8
+          if (col >= p.cols) continue;
+          uint32_t w[4];
+#pragma unroll
+          for (int j = 0; j < 8; j += 2)
+            w[j / 2] = bf16_bits_rn(0.0 + sum(j0 + j)) | ((uint32_t)bf16_bits_rn(0.0 + sum(j0 + j + 1)) << 16);
+          if (p.grad_by_row) {
+            *reinterpret_cast<uint4*>(p.grad + (int64_t)row * p.cols + col) = make_uint4(w[0], w[1], w[2], w[3]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) p.grad[(int64_t)(col + j) * p.rows + row] = (uint16_t)(w[j / 2] >> (16 * (j & 1)));
+          }
+        }
+      } else {
+        double* out = p.partial + (int64_t)split * p.cols * p.rows;
+#pragma unroll
+        for (int j = 0; j < HALF; ++j) {
+          const int col = col0 + c0 + j;
+          if (col < p.cols) out[(int64_t)col * p.rows + row] = sum(j);
+        }
       }
     }
     tc_fence_before();
@@ -365,26 +395,55 @@ __global__ void __launch_bounds__(LrCfg<BJ, TERMS, A8>::kThreads, 1)
   }
 }
 
-template <int BJ, int TERMS, bool A8 = false>
+template <int BJ, int TERMS>
+__global__ void __launch_bounds__(kLrThreads, 1) lowrank_kernel(const __grid_constant__ LowRankParams p) {
+  lowrank_block<BJ, TERMS, false>(p, blockIdx.x, blockIdx.y, blockIdx.z);
+}
+
+// The two gradients of a backward pass whose x is an 8-bit checkpoint, dA^T = x^T u and dB = dY^T t, in one
+// launch: neither reads what the other writes, and at a few hundred tokens a launch of its own costs
+// each more than its tiles.  Where the tokens are not split the blocks write the gradients themselves.
+struct LowRankPair {
+  LowRankParams a, b;
+  int32_t blocks_a;
+};
+
+template <int BJ>
+__global__ void __launch_bounds__(kLrA8Threads, 1) lowrank_pair_kernel(const __grid_constant__ LowRankPair p) {
+  const bool first = (int)blockIdx.x < p.blocks_a;
+  const int id = (int)blockIdx.x - (first ? 0 : p.blocks_a);
+  const int tiles_m = ((first ? p.a.rows : p.b.rows) + 127) / 128, tiles_n = (p.a.cols + BJ - 1) / BJ;
+  const int tile_row = id % tiles_m, rest = id / tiles_m;
+  if (first) lowrank_block<BJ, 3, true>(p.a, tile_row, rest % tiles_n, rest / tiles_n);
+  else lowrank_block<BJ, 3, false>(p.b, tile_row, rest % tiles_n, rest / tiles_n);
+}
+
+template <int BJ, int TERMS>
 static cudaError_t launch_lowrank_t(const LowRankParams& p, cudaStream_t st) {
-  using C = LrCfg<BJ, TERMS, A8>;
+  using C = LrCfg<BJ, TERMS>;
   static std::atomic<uint64_t> configured{0};
-  cudaError_t e = enable_smem_once(lowrank_kernel<BJ, TERMS, A8>, C::kSmemBytes, configured);
+  cudaError_t e = enable_smem_once(lowrank_kernel<BJ, TERMS>, C::kSmemBytes, configured);
   if (e != cudaSuccess) return e;
   dim3 grid((p.rows + 127) / 128, (p.cols + BJ - 1) / BJ, p.splits);
-  lowrank_kernel<BJ, TERMS, A8><<<grid, C::kThreads, C::kSmemBytes, st>>>(p);
+  lowrank_kernel<BJ, TERMS><<<grid, C::kThreads, C::kSmemBytes, st>>>(p);
   return cudaGetLastError();
 }
 
-// bj in {16, 32, 64}, terms in {1, 3} (3 with an 8-bit A operand)
+template <int BJ>
+static cudaError_t launch_lowrank_pair_t(LowRankPair& p, cudaStream_t st) {
+  constexpr int smem = LrCfg<BJ, 3, true>::kSmemBytes > LrCfg<BJ, 3>::kSmemBytes ? LrCfg<BJ, 3, true>::kSmemBytes
+                                                                                 : LrCfg<BJ, 3>::kSmemBytes;
+  static std::atomic<uint64_t> configured{0};
+  cudaError_t e = enable_smem_once(lowrank_pair_kernel<BJ>, smem, configured);
+  if (e != cudaSuccess) return e;
+  auto blocks = [&](const LowRankParams& q) { return (q.rows + 127) / 128 * ((q.cols + BJ - 1) / BJ) * q.splits; };
+  p.blocks_a = blocks(p.a);
+  lowrank_pair_kernel<BJ><<<p.blocks_a + blocks(p.b), kLrA8Threads, smem, st>>>(p);
+  return cudaGetLastError();
+}
+
+// bj in {16, 32, 64}, terms in {1, 3}
 static cudaError_t launch_lowrank(const LowRankParams& p, int bj, int terms, cudaStream_t st) {
-  if (p.a8_scales) {
-    if (terms != 3 || !p.a_mn) return cudaErrorInvalidValue;
-    if (bj == 16) return launch_lowrank_t<16, 3, true>(p, st);
-    if (bj == 32) return launch_lowrank_t<32, 3, true>(p, st);
-    if (bj == 64) return launch_lowrank_t<64, 3, true>(p, st);
-    return cudaErrorInvalidValue;
-  }
   if (terms == 1) {
     if (bj == 16) return launch_lowrank_t<16, 1>(p, st);
     if (bj == 32) return launch_lowrank_t<32, 1>(p, st);
@@ -397,13 +456,17 @@ static cudaError_t launch_lowrank(const LowRankParams& p, int bj, int terms, cud
   return cudaErrorInvalidValue;
 }
 
+// a: an 8-bit A operand, b: a bf16 one; both MN-major with three terms and the same columns.
+static cudaError_t launch_lowrank_pair(LowRankPair& p, int bj, cudaStream_t st) {
+  if (bj == 16) return launch_lowrank_pair_t<16>(p, st);
+  if (bj == 32) return launch_lowrank_pair_t<32>(p, st);
+  if (bj == 64) return launch_lowrank_pair_t<64>(p, st);
+  return cudaErrorInvalidValue;
+}
+
 // ---------------------------------------------------------------------------------------
 // finalize kernels
 // ---------------------------------------------------------------------------------------
-__device__ __forceinline__ uint16_t bf16_bits_rn(double v) {
-  return __bfloat16_as_ushort(__float2bfloat16_rn((float)v));
-}
-
 // Three bf16 terms of v: t1 = bf16(v), t2 = bf16(v - t1), t3 = bf16(v - t1 - t2), each
 // difference formed in float64.  For an fp32 v the three terms are exact (8 + 8 + 8 bits).
 __device__ __forceinline__ void split3(double v, uint16_t& a, uint16_t& b, uint16_t& c) {
@@ -471,11 +534,10 @@ __global__ void finalize_tokens_kernel(const double* __restrict__ partial, int s
   }
 }
 
-// fp32 t [M][r] -> exact three-term split, transposed: T3[term][j][m].
-__global__ void split3_T_kernel(const float* __restrict__ t, int64_t M, int64_t r, uint16_t* __restrict__ T3,
-                                int64_t ldT) {
+// fp32 t [M][r] -> exact three-term split, transposed: T3[term][j][m]; one 32 x 32 tile by 32 x 8 threads.
+__device__ __forceinline__ void split3_T_tile(const float* __restrict__ t, int64_t M, int64_t r,
+                                              uint16_t* __restrict__ T3, int64_t ldT, int64_t m0, int64_t j0) {
   __shared__ float tile[32][33];
-  const int64_t m0 = (int64_t)blockIdx.y * 32, j0 = (int64_t)blockIdx.x * 32;
   for (int i = threadIdx.y; i < 32; i += blockDim.y) {
     const int64_t m = m0 + i, j = j0 + threadIdx.x;
     tile[i][threadIdx.x] = (m < M && j < r) ? t[m * r + j] : 0.0f;
@@ -493,14 +555,26 @@ __global__ void split3_T_kernel(const float* __restrict__ t, int64_t M, int64_t 
   }
 }
 
+__global__ void split3_T_kernel(const float* __restrict__ t, int64_t M, int64_t r, uint16_t* __restrict__ T3,
+                                int64_t ldT) {
+  split3_T_tile(t, M, r, T3, ldT, (int64_t)blockIdx.y * 32, (int64_t)blockIdx.x * 32);
+}
+
+// Both operands that a backward pass lays out anew, in one launch: B [N][r] -> B^T [r][N], and t as above.
+__global__ void bwd_operands_kernel(const uint16_t* __restrict__ B, int64_t N, int64_t r, uint16_t* __restrict__ Bt,
+                                    const float* __restrict__ t, int64_t M, uint16_t* __restrict__ T3, int64_t ldT) {
+  const int64_t tiles_n = (N + 31) / 32, j0 = (int64_t)blockIdx.y * 32;
+  if ((int64_t)blockIdx.x < tiles_n) transpose_bf16_tile(B, N, r, Bt, N, (int64_t)blockIdx.x * 32, j0);
+  else split3_T_tile(t, M, r, T3, ldT, ((int64_t)blockIdx.x - tiles_n) * 32, j0);
+}
+
 // Feature-side gradient: g[j][i] = bf16(sum_z partial[z][j][i]); transpose_out = 0 writes
 // out[j * n + i] (dA, [r][K]), 1 writes out[i * r + j] (dB, [N][r]).  One tile of 32 rows x 8 columns
 // (i0.., j0..) per block of 32 x 8 threads; the transposed case goes through shared memory so that
 // both the partials and the output are accessed along their rows.
-__global__ void finalize_grad_kernel(const double* __restrict__ partial, int splits, int64_t r, int64_t n,
-                                     uint16_t* __restrict__ out, int transpose_out) {
+__device__ __forceinline__ void finalize_grad_tile(const double* __restrict__ partial, int splits, int64_t r, int64_t n,
+                                                   uint16_t* __restrict__ out, int transpose_out, int64_t i0, int64_t j0) {
   __shared__ uint16_t tile[8][34];
-  const int64_t i0 = (int64_t)blockIdx.x * 32, j0 = (int64_t)blockIdx.y * 8;
   {
     const int64_t j = j0 + threadIdx.y, i = i0 + threadIdx.x;
     uint16_t g = 0;
@@ -518,6 +592,24 @@ __global__ void finalize_grad_kernel(const double* __restrict__ partial, int spl
   if (i < n && j < r) out[i * r + j] = tile[t & 7][t >> 3];
 }
 
+__global__ void finalize_grad_kernel(const double* __restrict__ partial, int splits, int64_t r, int64_t n,
+                                     uint16_t* __restrict__ out, int transpose_out) {
+  finalize_grad_tile(partial, splits, r, n, out, transpose_out, (int64_t)blockIdx.x * 32, (int64_t)blockIdx.y * 8);
+}
+
+// dA (not transposed) and dB (transposed) of a paired launch.
+struct GradJob {
+  const double* partial;
+  int32_t splits;
+  int64_t n;
+  uint16_t* out;
+};
+__global__ void finalize_grads_kernel(const GradJob a, const GradJob b, int64_t r) {
+  const int64_t tiles_a = (a.n + 31) / 32, tile = blockIdx.x, j0 = (int64_t)blockIdx.y * 8;
+  if (tile < tiles_a) finalize_grad_tile(a.partial, a.splits, r, a.n, a.out, 0, tile * 32, j0);
+  else finalize_grad_tile(b.partial, b.splits, r, b.n, b.out, 1, (tile - tiles_a) * 32, j0);
+}
+
 static cudaError_t launch_finalize_tokens(const double* partial, int splits, int64_t M, int64_t r, double alpha,
                                           float* f32, uint16_t* hi, uint16_t* lo, uint16_t* T3, int64_t ldT,
                                           cudaStream_t st) {
@@ -530,6 +622,19 @@ static cudaError_t launch_split3_T(const float* t, int64_t M, int64_t r, uint16_
                                    cudaStream_t st) {
   dim3 grid((unsigned)((r + 31) / 32), (unsigned)((M + 31) / 32));
   split3_T_kernel<<<grid, dim3(32, 8), 0, st>>>(t, M, r, T3, ldT);
+  return cudaGetLastError();
+}
+
+static cudaError_t launch_bwd_operands(const uint16_t* B, int64_t N, int64_t r, uint16_t* Bt, const float* t, int64_t M,
+                                       uint16_t* T3, int64_t ldT, cudaStream_t st) {
+  dim3 grid((unsigned)((N + 31) / 32 + (M + 31) / 32), (unsigned)((r + 31) / 32));
+  bwd_operands_kernel<<<grid, dim3(32, 8), 0, st>>>(B, N, r, Bt, t, M, T3, ldT);
+  return cudaGetLastError();
+}
+
+static cudaError_t launch_finalize_grads(const GradJob& a, const GradJob& b, int64_t r, cudaStream_t st) {
+  dim3 grid((unsigned)((a.n + 31) / 32 + (b.n + 31) / 32), (unsigned)((r + 7) / 8));
+  finalize_grads_kernel<<<grid, dim3(32, 8), 0, st>>>(a, b, r);
   return cudaGetLastError();
 }
 

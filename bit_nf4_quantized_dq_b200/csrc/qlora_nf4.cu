@@ -208,16 +208,23 @@ FwdPlan plan_fwd(const LinearShape& s) {
 struct BwdPlan {
   int bn, splits;      // fused dX
   LowRankPlan u, a, b; // u = s dY B, dA, dB
+  bool paired;         // dA and dB in one launch, with the same splits of the tokens
 };
 
-BwdPlan plan_bwd(const LinearShape& s) {
+// `paired`: the backward pass from an 8-bit x
+BwdPlan plan_bwd(const LinearShape& s, bool paired = false) {
   BwdPlan p;
+  p.paired = paired;
   p.bn = bn_for(s.M);
   const int64_t tiles = ((s.K + 127) / 128) * ((s.M + p.bn - 1) / p.bn);
   p.splits = choose_splits(tiles, kblocks(s.N));
   p.u = plan_lowrank(s.M, s.r, s.N);
   p.a = plan_lowrank(s.K, s.r, s.M);
   p.b = plan_lowrank(s.N, s.r, s.M);
+  if (paired) {
+    const int64_t both = ((s.K + 127) / 128 + (s.N + 127) / 128) * ((s.r + p.a.bj - 1) / p.a.bj);
+    p.a.splits = p.b.splits = choose_splits(both, kblocks(s.M));
+  }
   return p;
 }
 
@@ -262,8 +269,8 @@ size_t bwd_carve(Carver& c, const LinearShape& s, const BwdPlan& p, BwdWs* w) {
   w->uT3 = c.take<uint16_t>((size_t)3 * s.r * ldM);
   w->tT3 = c.take<uint16_t>((size_t)3 * s.r * ldM);
   size_t np = (size_t)p.u.splits * s.r * s.M;
-  np = std::max(np, (size_t)p.a.splits * s.r * s.K);
-  np = std::max(np, (size_t)p.b.splits * s.r * s.N);
+  const size_t na = (size_t)p.a.splits * s.r * s.K, nb = (size_t)p.b.splits * s.r * s.N;
+  np = std::max(np, p.paired ? na + nb : std::max(na, nb));
   w->partial = c.take<double>(np);
   w->partX = p.splits > 1 ? c.take<float>((size_t)p.splits * s.M * s.K) : nullptr;
   return c.off;
@@ -272,11 +279,11 @@ size_t bwd_carve(Carver& c, const LinearShape& s, const BwdPlan& p, BwdWs* w) {
 // One low-rank product: A operand map (K-major over [rows][k] or MN-major over [k][rows]),
 // `terms` B maps over [r][k] (K-major), fp64 partials into `partial`.
 // With `a8_scales` the A operand is an 8-bit checkpoint's codes (MN-major, [k][rows]).
-int run_lowrank(const void* a_base, bool a_mn, int64_t a_inner, int64_t a_outer, int64_t a_pitch_bytes,
-                const uint16_t* const* b_terms, int terms, int64_t b_inner, int64_t b_pitch_bytes, int r,
-                int64_t rows, int64_t kdim, const LowRankPlan& pl, double* partial, cudaStream_t st,
-                const uint8_t* a8_scales = nullptr) {
-  qnf4::LowRankParams lp;
+int lowrank_params(qnf4::LowRankParams* out, const void* a_base, bool a_mn, int64_t a_inner, int64_t a_outer,
+                   int64_t a_pitch_bytes, const uint16_t* const* b_terms, int terms, int64_t b_inner,
+                   int64_t b_pitch_bytes, int r, int64_t rows, int64_t kdim, const LowRankPlan& pl, double* partial,
+                   const uint8_t* a8_scales = nullptr) {
+  qnf4::LowRankParams& lp = *out;
   memset(&lp, 0, sizeof(lp));
   if (a8_scales) {
     if (int rc = make_map(&lp.a_map, a_base, false, a_inner, a_outer, a_pitch_bytes, 128, 64)) return rc;
@@ -298,6 +305,16 @@ int run_lowrank(const void* a_base, bool a_mn, int64_t a_inner, int64_t a_outer,
   lp.rows = (int32_t)rows;
   lp.cols = r;
   lp.partial = partial;
+  return QNF4_OK;
+}
+
+int run_lowrank(const void* a_base, bool a_mn, int64_t a_inner, int64_t a_outer, int64_t a_pitch_bytes,
+                const uint16_t* const* b_terms, int terms, int64_t b_inner, int64_t b_pitch_bytes, int r,
+                int64_t rows, int64_t kdim, const LowRankPlan& pl, double* partial, cudaStream_t st) {
+  qnf4::LowRankParams lp;
+  if (int rc = lowrank_params(&lp, a_base, a_mn, a_inner, a_outer, a_pitch_bytes, b_terms, terms, b_inner, b_pitch_bytes,
+                              r, rows, kdim, pl, partial))
+    return rc;
   cudaError_t e = qnf4::launch_lowrank(lp, pl.bj, terms, st);
   if (e != cudaSuccess) return cuda_fail(e, "low-rank launch");
   return QNF4_OK;
@@ -953,7 +970,7 @@ int linear_bwd_impl(const uint16_t* dY, const void* x, const uint8_t* x_scales, 
       !aligned(t_saved, 16) || !aligned(dA, 16) || !aligned(dB, 16) || (dX && !aligned(dX, 16)) ||
       !aligned(workspace, 256))
     return fail(QNF4_ERR_UNSUPPORTED, "alignment: operands 16 B, workspace 256 B");
-  const BwdPlan plan = plan_bwd(sh);
+  const BwdPlan plan = plan_bwd(sh, x_scales != nullptr);
   Carver c{static_cast<char*>(workspace)};
   BwdWs w;
   const size_t need = bwd_carve(c, sh, plan, &w);
@@ -964,10 +981,15 @@ int linear_bwd_impl(const uint16_t* dY, const void* x, const uint8_t* x_scales, 
   mark(0, st);
 
   // 1) B^T [r][N]; t split into three exact bf16 terms, transposed [3][r][M]
-  e = qnf4::launch_transpose_bf16(B, N, r, w.Bt, N, st);
-  if (e != cudaSuccess) return cuda_fail(e, "transpose launch");
-  e = qnf4::launch_split3_T(t_saved, M, r, w.tT3, ldM, st);
-  if (e != cudaSuccess) return cuda_fail(e, "split launch");
+  if (x_scales) {
+    e = qnf4::launch_bwd_operands(B, N, r, w.Bt, t_saved, M, w.tT3, ldM, st);
+    if (e != cudaSuccess) return cuda_fail(e, "operand launch");
+  } else {
+    e = qnf4::launch_transpose_bf16(B, N, r, w.Bt, N, st);
+    if (e != cudaSuccess) return cuda_fail(e, "transpose launch");
+    e = qnf4::launch_split3_T(t_saved, M, r, w.tT3, ldM, st);
+    if (e != cudaSuccess) return cuda_fail(e, "split launch");
+  }
   mark(1, st);
 
   // 2) u = s dY B (float64-accumulated): hi / lo [M][r] for dX, three terms [3][r][M] for dA
@@ -1020,20 +1042,37 @@ int linear_bwd_impl(const uint16_t* dY, const void* x, const uint8_t* x_scales, 
     }
   }
   mark(3, st);
-  // 4) dA^T = x^T u (u as three terms), reduced over the M tokens
-  {
-    const uint16_t* bt[3] = {w.uT3, w.uT3 + (size_t)r * ldM, w.uT3 + (size_t)2 * r * ldM};
-    const int64_t pitch = x_scales ? qnf4::a8_ld(K) : K * 2;
-    if (int rc = run_lowrank(x, true, K, M, pitch, bt, 3, M, ldM * 2, r, K, M, plan.a, w.partial, st, x_scales))
+  // dA^T = x^T u and dB = dY^T t (u and t as three terms), reduced over the M tokens
+  const uint16_t* ut[3] = {w.uT3, w.uT3 + (size_t)r * ldM, w.uT3 + (size_t)2 * r * ldM};
+  const uint16_t* tt[3] = {w.tT3, w.tT3 + (size_t)r * ldM, w.tT3 + (size_t)2 * r * ldM};
+  if (x_scales) {
+    // 4) both at once, and where the tokens are split the sums of the splits
+    double* part_b = w.partial + (size_t)plan.a.splits * r * K;
+    qnf4::LowRankPair lp;
+    if (int rc = lowrank_params(&lp.a, x, true, K, M, qnf4::a8_ld(K), ut, 3, M, ldM * 2, r, K, M, plan.a, w.partial,
+                                x_scales))
       return rc;
+    if (int rc = lowrank_params(&lp.b, dY, true, N, M, N * 2, tt, 3, M, ldM * 2, r, N, M, plan.b, part_b)) return rc;
+    if (plan.a.splits == 1) {
+      lp.a.grad = dA;
+      lp.b.grad = dB;
+      lp.b.grad_by_row = 1;
+    }
+    e = qnf4::launch_lowrank_pair(lp, plan.a.bj, st);
+    if (e != cudaSuccess) return cuda_fail(e, "low-rank launch");
+    mark(4, st);
+    if (plan.a.splits > 1)
+      e = qnf4::launch_finalize_grads(qnf4::GradJob{w.partial, plan.a.splits, K, dA},
+                                      qnf4::GradJob{part_b, plan.b.splits, N, dB}, r, st);
+    if (e != cudaSuccess) return cuda_fail(e, "dA, dB finalize launch");
+  } else {
+    // 4) dA
+    if (int rc = run_lowrank(x, true, K, M, K * 2, ut, 3, M, ldM * 2, r, K, M, plan.a, w.partial, st)) return rc;
     e = qnf4::launch_finalize_grad(w.partial, plan.a.splits, r, K, dA, 0, st);
     if (e != cudaSuccess) return cuda_fail(e, "dA finalize launch");
-  }
-  mark(4, st);
-  // 5) dB = dY^T t (t as three terms), reduced over the M tokens
-  {
-    const uint16_t* bt[3] = {w.tT3, w.tT3 + (size_t)r * ldM, w.tT3 + (size_t)2 * r * ldM};
-    if (int rc = run_lowrank(dY, true, N, M, N * 2, bt, 3, M, ldM * 2, r, N, M, plan.b, w.partial, st)) return rc;
+    mark(4, st);
+    // 5) dB
+    if (int rc = run_lowrank(dY, true, N, M, N * 2, tt, 3, M, ldM * 2, r, N, M, plan.b, w.partial, st)) return rc;
     e = qnf4::launch_finalize_grad(w.partial, plan.b.splits, r, N, dB, 1, st);
     if (e != cudaSuccess) return cuda_fail(e, "dB finalize launch");
   }
@@ -1048,9 +1087,9 @@ extern "C" {
 size_t qlora_linear_bwd_workspace_bytes(int64_t M, int64_t K, int64_t N, int r) {
   LinearShape s{M, K, N, r};
   if (M <= 0 || K <= 0 || N <= 0 || r <= 0) return 0;
-  Carver c{nullptr};
+  Carver c{nullptr}, c8{nullptr};
   BwdWs w;
-  return bwd_carve(c, s, plan_bwd(s), &w);
+  return std::max(bwd_carve(c, s, plan_bwd(s), &w), bwd_carve(c8, s, plan_bwd(s, true), &w));   // x in either form
 }
 
 int qlora_linear_bwd(const uint16_t* dY, const uint16_t* x, const float* t_saved, int64_t M, int64_t K, int64_t N,
