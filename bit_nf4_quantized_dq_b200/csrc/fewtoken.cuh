@@ -45,7 +45,9 @@ constexpr int kFewItemBytes = 16 * kFewCols / 2;
 constexpr int kFewRingBytes = kFewWarps * kFewRing * kFewItemBytes;
 constexpr int kFewSmemBytes = (int)kFewRingAddr + kFewRingBytes + kFewWarps * kFewRing * 8 + 16;
 static_assert(kFewSmemBytes <= 227 * 1024, "shared memory of one block");
-constexpr int kFewRaggedSmemBytes = (int)kFewRingAddr;
+constexpr int kFewStageBytes = 4 * kFewCols * 2;   // x of four tokens
+constexpr int kFewRaggedSmemBytes = (int)kFewRingAddr + kFewWarps * kFewStageBytes;
+static_assert(kFewStageBytes <= kFewItemBytes, "a slot of the ring hands over x");
 // Room for sums: the block's part of shared memory starts 1 KB up.  (The kernels measure it, and take
 // their tiles in more rounds if there is less.)
 constexpr int kFewSumBytes = 63 * 1024;
@@ -146,33 +148,56 @@ __device__ __forceinline__ float few_scale_value(const FewTokenParams& p, const 
   return p.scale_fp32 ? s.value : dq_block_scale(s.code, s.value, mean);
 }
 
-// Fills the table: warp w writes the pairs of the bytes w, w + kFewWarps, ...; `stage` holds 16 floats
-// that nothing else uses yet.  Returns the lane's table address, which every lookup's address
-// depends on (opaque, so that no lookup moves in front of the barrier).
-__device__ __forceinline__ uint32_t few_fill_table(const FewTokenParams& p, uint8_t* table, float* stage) {
-  const int lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) {
+// Fills the table: warp w writes the pairs of the bytes w, w + 16, ..., whose low code is w.  Returns the
+// lane's table address, which every lookup's address depends on (opaque, so that no lookup moves in
+// front of the barrier).
+__device__ __forceinline__ uint32_t few_fill_table(const FewTokenParams& p, uint8_t* table) {
+  static_assert(kFewWarps == 16, "one warp per low code");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const float low = p.cb.q[warp];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) stage[j] = p.cb.q[j];
-  }
-  __syncthreads();
-  for (int b = threadIdx.x >> 5; b < 256; b += kFewWarps)
-    *reinterpret_cast<float2*>(table + b * 256 + lane * 8) = make_float2(stage[b & 15], stage[b >> 4]);
+  for (int i = 0; i < 16; ++i)
+    *reinterpret_cast<float2*>(table + (16 * i + warp) * 256 + lane * 8) = make_float2(low, p.cb.q[i]);
   __syncthreads();
   uint32_t lane_addr = kFewTableAddr + (uint32_t)lane * 8u;
   asm volatile("" : "+r"(lane_addr)::"memory");
   return lane_addr;
 }
-// Eight codes -> four bf16 pairs of the dequantized weight.
-__device__ __forceinline__ void few_expand8(uint32_t w, float scale, uint32_t lane_addr, uint32_t (&o)[4]) {
+// Brings `bytes` bytes into L2, a line per thread.  What the end of a block reads (the adapter's rows, bias,
+// residual) is fetched from its start on: read on demand it cost 1 to 2 us there, of 10.
+__device__ __forceinline__ void few_prefetch(const void* base, int64_t bytes, int index, int threads) {
+  const char* at = static_cast<const char*>(base);
+  if (bytes <= 0) return;
+  for (int64_t o = (int64_t)index * 128; o < bytes + 127; o += (int64_t)threads * 128)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(at + (o < bytes ? o : bytes - 1)));
+}
+__device__ __forceinline__ void few_prefetch_rows(const FewTokenParams& p, int64_t n0, int64_t n1, bool outputs) {
+  if (p.t) few_prefetch(p.B + n0 * p.r, (n1 - n0) * p.r * 2, threadIdx.x, 32 * kFewWarps);
+  if (!outputs) return;
+  if (p.post.bias && threadIdx.x < 32) few_prefetch(p.post.bias + n0, (n1 - n0) * 2, threadIdx.x, 32);
+  if (p.post.residual)
+    for (int tok = threadIdx.x >> 5; tok < p.M; tok += kFewWarps)
+      few_prefetch(p.post.residual + tok * p.N + n0, (n1 - n0) * 2, threadIdx.x & 31, 32);
+}
+// Eight codes -> the four level pairs; and those times the scale, as bf16 pairs of the dequantized weight.
+__device__ __forceinline__ void few_lookup8(uint32_t w, uint32_t lane_addr, uint64_t (&q)[4]) {
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const uint32_t at = prmt(w, lane_addr, 0x7604u | ((uint32_t)k << 4));
-    uint64_t q;
-    asm("ld.shared.b64 %0, [%1];" : "=l"(q) : "r"(at));   // the table does not change any more
-    q = f32x2_mul(q, f32_pair(scale, scale));
-    o[k] = pack_bf16x2(pair_lo(q), pair_hi(q));
+    asm("ld.shared.b64 %0, [%1];" : "=l"(q[k]) : "r"(at));   // the table does not change any more
   }
+}
+__device__ __forceinline__ void few_round8(const uint64_t (&q)[4], uint64_t scale, uint32_t (&o)[4]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint64_t v = f32x2_mul(q[k], scale);
+    o[k] = pack_bf16x2(pair_lo(v), pair_hi(v));
+  }
+}
+__device__ __forceinline__ void few_expand8(uint32_t w, float scale, uint32_t lane_addr, uint32_t (&o)[4]) {
+  uint64_t q[4];
+  few_lookup8(w, lane_addr, q);
+  few_round8(q, f32_pair(scale, scale), o);
 }
 
 // A block's share of `tiles`, and its rounds of even sizes whose sums (`slot` floats per item, `quads`
@@ -185,10 +210,53 @@ __device__ __forceinline__ FewShare few_share(const float* sums, int tiles, int 
   FewShare s;
   s.begin = (int)blockIdx.x * base + min((int)blockIdx.x, extra);
   s.end = s.begin + base + ((int)blockIdx.x < extra ? 1 : 0);
-  const int most = (int)(kFewTableAddr - smem_u32(sums)) / (4 * slot * (quads + 1));
-  const int rounds = (s.end - s.begin + most - 1) / most;
-  s.per_round = (s.end - s.begin + rounds - 1) / rounds;
+  s.per_round = s.end - s.begin;
+  const int room = (int)(kFewTableAddr - smem_u32(sums)), one = 4 * slot * (quads + 1);
+  if ((int64_t)s.per_round * one > room) {   // (the divisions are not free at the start of a short kernel)
+    const int most = room / one, rounds = (s.per_round + most - 1) / most;
+    s.per_round = (s.per_round + rounds - 1) / rounds;
+  }
   return s;
+}
+
+// This lane's 64 columns (64 c .. 64 c + 63 of the quad) of its tokens g and, with NT = 2, g + 8, zeros
+// past K.  Read directly, an instruction asks for 16 bytes of 32 different lines; so the warp reads whole
+// rows of 512 bytes, four tokens at a time, and hands them over through 2 KB of shared memory: 16-byte
+// piece j of lane column c of row i lies at j ^ (c + 4 i), so that neither side meets a bank conflict.
+// 13824 x 5120, 8 tokens: 25.5 us, direct 28.6; 5120 x 13816 (ragged), 8 tokens 38.5 and 45.4, 16 tokens
+// 63.7 and 80.  Tokens past M keep what the buffer held; nothing reads their sums.
+template <int NT>
+__device__ __forceinline__ void few_load_x(const FewTokenParams& p, int quad, uint8_t* stage, uint4 (&xv)[NT][8]) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  const int64_t col = (int64_t)quad * kFewCols + 8 * lane;
+  const uint16_t* src = p.x + col;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    uint4 raw[2][4];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int tok = 8 * t + 4 * k + i;
+        raw[k][i] = make_uint4(0u, 0u, 0u, 0u);
+        if (tok < p.M && col < p.K) raw[k][i] = __ldg(reinterpret_cast<const uint4*>(src + tok * p.K));
+      }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (8 * t + 4 * k >= p.M) break;
+      __syncwarp();   // the buffer's last readers are done
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint4*>(stage + i * 512 + (((lane & 24) | ((lane & 7) ^ (((lane >> 3) + 4 * i) & 7))) << 4)) =
+            raw[k][i];
+      __syncwarp();
+      if ((g >> 2) == k) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          xv[t][j] = *reinterpret_cast<const uint4*>(stage + (g & 3) * 512 + ((8 * c + (j ^ ((c + 4 * g) & 7))) << 4));
+      }
+    }
+  }
 }
 
 // The outputs of a round's tiles: the items' sums added over the columns in order (and the adapter
@@ -230,13 +298,13 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) few_token_kernel(const __gr
   uint64_t* const bars = reinterpret_cast<uint64_t*>(smem0 + kFewRingAddr + kFewRingBytes);
   uint64_t* const full = bars + warp * kFewRing;
   volatile uint32_t* const abort_word = reinterpret_cast<uint32_t*>(bars + kFewWarps * kFewRing);
-  if (threadIdx.x < kFewWarps * kFewRing) mbar_init(&bars[threadIdx.x], 1);
-  if (threadIdx.x == 0) {
-    *abort_word = 0u;
-    tma_prefetch_desc(&p.map);
+  if (threadIdx.x == 0) tma_prefetch_desc(&p.map);
+  if (lane == 0) {   // a warp's ring is its own: no barrier of the block
+    for (int k = 0; k < kFewRing; ++k) mbar_init(&full[k], 1);
+    mbar_fence_init();
   }
-  mbar_fence_init();
-  __syncthreads();
+  if (threadIdx.x == 0) *abort_word = 0u;
+  __syncwarp();
 
   const int quads = (int)((p.K + kFewCols - 1) / kFewCols);
   const int tiles = (int)((p.N + kRows - 1) / kRows);
@@ -280,7 +348,30 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) few_token_kernel(const __gr
         ++c_quad;
       }
     };
-    for (int k = 0, s = slot; k < kFewRing; ++k, s = s + 1 == kFewRing ? 0 : s + 1) load_codes(s);
+    // The first loads go out as one instruction of as many lanes (an instruction holds its thread for
+    // hundreds of cycles, whatever the number of its lanes).
+    {
+      const int ahead = min(kFewRing - 1, c_left);   // the last slot hands over x first
+      const int to = slot + lane < kFewRing ? slot + lane : slot + lane - kFewRing;
+      int my_quad = c_quad, my_tile = c_tile;
+      for (int k = 0; k < ahead; ++k) {
+        if (k == lane) {
+          my_quad = c_quad;
+          my_tile = c_tile;
+        }
+        if (++c_tile == nt) {
+          c_tile = 0;
+          ++c_quad;
+        }
+      }
+      if (lane < ahead) {
+        mbar_arrive_expect_tx(&full[to], kFewItemBytes);
+        tma_load_2d(ring + to * kFewItemBytes, &p.map, my_quad * (kFewCols / 2), (t0 + my_tile) * kRows, &full[to]);
+      }
+      c_left -= ahead;
+      pending = ahead;
+      __syncwarp();
+    }
     // The scales of the next item.  Columns past K (whose codes arrive as zeros, and where x is zero) and
     // rows past N (N is a multiple of 8; their sums are not used) take the scales before them.
     int f_quad = quad, f_tile = tile;
@@ -314,17 +405,36 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) few_token_kernel(const __gr
       fetch();
     }
     uint4 xv[NT][8];
-    auto load_x = [&]() {   // this lane's 64 columns of its tokens; tokens past M repeat the last one, unread
-      const int64_t col = (int64_t)quad * kFewCols + 64 * c;
+    // x by way of a free slot of the ring, which then takes its codes; with two groups of tokens each lane
+    // reads its own (their registers leave no room for rows on their way: 44.8 us instead of 42.8 for 16
+    // tokens of 13824 x 5120)
+    auto load_x = [&](int s) {
+      if constexpr (TWO) {
+        load_codes(s);
+        const int64_t col = (int64_t)quad * kFewCols + 64 * c;
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const uint4* src = reinterpret_cast<const uint4*>(p.x + (int64_t)min(8 * t + g, p.M - 1) * p.K + col);
+        for (int t = 0; t < NT; ++t) {   // tokens past M repeat the last one, unread
+          const uint4* src = reinterpret_cast<const uint4*>(p.x + (int64_t)min(8 * t + g, p.M - 1) * p.K + col);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) xv[t][j] = col < p.K ? __ldg(src + j) : make_uint4(0u, 0u, 0u, 0u);
+          for (int j = 0; j < 8; ++j) xv[t][j] = col < p.K ? __ldg(src + j) : make_uint4(0u, 0u, 0u, 0u);
+        }
+      } else {
+        few_load_x<NT>(p, quad, ring + s * kFewItemBytes, xv);
+        fence_proxy_async_smem();
+        __syncwarp();
+        load_codes(s);
       }
     };
-    if (i0 < i1) load_x();
-    if (lane_addr == 0u) lane_addr = few_fill_table(p, smem0 + kFewTableAddr, sums);   // while the codes arrive
+    if (i0 < i1) load_x(slot == 0 ? kFewRing - 1 : slot - 1);
+    if (lane_addr == 0u) {   // while the codes arrive
+      lane_addr = few_fill_table(p, smem0 + kFewTableAddr);
+      if constexpr (FLAT) {
+        const int64_t tile16 = (int64_t)blockIdx.x * kFewWarps;
+        few_prefetch_rows(p, min(tile16 * kRows, p.N), min((tile16 + kFewWarps) * kRows, p.N), false);
+      } else {
+        few_prefetch_rows(p, (int64_t)share.begin * kRows, min((int64_t)share.end * kRows, p.N), true);
+      }
+    }
     for (int i = i0; i < i1 && ok;) {
       // this warp's tiles of one quad of columns
       const int stop = min(i1, i + nt - tile);
@@ -338,33 +448,46 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) few_token_kernel(const __gr
         // rows g and g + 8: their 16-byte chunks 2 c and 2 c + 1 lie at (chunk ^ g), a phase of 8 lanes (two
         // rows) reads 8 different bank groups
         const uint8_t* row = ring + slot * kFewItemBytes + g * 128;
-        const float v0 = few_scale_value(p, s0, mean), v1 = few_scale_value(p, s1, mean);
+        const float f0 = few_scale_value(p, s0, mean), f1 = few_scale_value(p, s1, mean);
         float acc[NT][2][4];
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int k = 0; k < 4; ++k) acc[t][0][k] = acc[t][1][k] = 0.0f;
+        uint4 qa[2], qb[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint4 qa = *reinterpret_cast<const uint4*>(row + (((2 * c + h) ^ g) << 4));
-          const uint4 qb = *reinterpret_cast<const uint4*>(row + 1024 + (((2 * c + h) ^ g) << 4));
-          const uint32_t wa[4] = {qa.x, qa.y, qa.z, qa.w}, wb[4] = {qb.x, qb.y, qb.z, qb.w};
+          qa[h] = *reinterpret_cast<const uint4*>(row + (((2 * c + h) ^ g) << 4));
+          qb[h] = *reinterpret_cast<const uint4*>(row + 1024 + (((2 * c + h) ^ g) << 4));
+        }
+        const uint32_t wa[8] = {qa[0].x, qa[0].y, qa[0].z, qa[0].w, qa[1].x, qa[1].y, qa[1].z, qa[1].w};
+        const uint32_t wb[8] = {qb[0].x, qb[0].y, qb[0].z, qb[0].w, qb[1].x, qb[1].y, qb[1].z, qb[1].w};
+        const uint64_t v0 = f32_pair(f0, f0), v1 = f32_pair(f1, f1);
+        // the lookups of the next 8 columns are on their way while these are rounded and multiplied
+        uint64_t la[2][4], lb[2][4];
+        few_lookup8(wa[0], lane_addr, la[0]);
+        few_lookup8(wb[0], lane_addr, lb[0]);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t a[4], b[4];
-            few_expand8(wa[j], v0, lane_addr, a);
-            few_expand8(wb[j], v1, lane_addr, b);
+        for (int j = 0; j < 8; ++j) {
+          if (j < 7) {
+            few_lookup8(wa[j + 1], lane_addr, la[(j + 1) & 1]);
+            few_lookup8(wb[j + 1], lane_addr, lb[(j + 1) & 1]);
+          }
+          uint32_t a[4], b[4];
+          few_round8(la[j & 1], v0, a);
+          few_round8(lb[j & 1], v1, b);
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              const uint4& x = xv[t][4 * h + j];
-              mma_bf16_16816(acc[t][0], a[0], b[0], a[1], b[1], x.x, x.y);
-              mma_bf16_16816(acc[t][1], a[2], b[2], a[3], b[3], x.z, x.w);
-            }
+          for (int t = 0; t < NT; ++t) {
+            const uint4& x = xv[t][j];
+            mma_bf16_16816(acc[t][0], a[0], b[0], a[1], b[1], x.x, x.y);
+            mma_bf16_16816(acc[t][1], a[2], b[2], a[3], b[3], x.z, x.w);
           }
         }
         --pending;
         __syncwarp();   // every lane has used its codes: the slot takes the item kFewRing ahead
-        load_codes(slot);
+        const int used = slot;
+        const bool turn = i + 1 == stop && stop < i1;   // to the next quad of columns
+        if (!turn) load_codes(used);
         if (++slot == kFewRing) {
           slot = 0;
           phase ^= 1u;
@@ -384,10 +507,12 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) few_token_kernel(const __gr
           }
         }
         if constexpr (FLAT) ++tile;
+        if (turn) {
+          ++quad;
+          load_x(used);
+        }
       }
-      ++quad;
       tile = 0;
-      if (i < i1) load_x();
     }
     if (p.t) {
       // t B^T: t as bf16 hi + lo (16 significant bits), one more slot of sums per tile
@@ -494,9 +619,9 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) few_token_ragged_kernel(con
   const int quads = (int)((p.K + kFewCols - 1) / kFewCols);
   const FewShare share = few_share(sums, (int)(p.N / kRows), quads, kSlot);
   const float mean = p.scale_fp32 ? 0.0f : __ldg(p.mean);
-  const uint16_t* x0 = p.x + (int64_t)min(g, p.M - 1) * p.K;       // rows past M repeat the last one, unread
-  const uint16_t* x1 = p.x + (int64_t)min(g + 8, p.M - 1) * p.K;
-  const uint32_t lane_addr = few_fill_table(p, few_smem + (kFewTableAddr - smem_u32(few_smem)), sums);
+  uint8_t* const stage = few_smem + (kFewRingAddr - smem_u32(few_smem)) + warp * kFewStageBytes;   // hands over x
+  few_prefetch_rows(p, (int64_t)share.begin * kRows, (int64_t)share.end * kRows, true);
+  const uint32_t lane_addr = few_fill_table(p, few_smem + (kFewTableAddr - smem_u32(few_smem)));
 
   for (int t0 = share.begin; t0 < share.end; t0 += share.per_round) {
     const int nt = min(share.end - t0, share.per_round);
@@ -535,17 +660,10 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) few_token_ragged_kernel(con
     }
     for (int i = i0; i < i1; ++quad, tile = 0) {
       // this warp's tiles of one quad of columns: x stays in registers
-      uint4 xa[8], xb[TWO ? 8 : 1];
-      const int64_t col = (int64_t)quad * kFewCols + 64 * c;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        xa[j] = make_uint4(0u, 0u, 0u, 0u);
-        if constexpr (TWO) xb[j] = xa[j];
-        if (col + 8 * j < p.K) {
-          xa[j] = __ldg(reinterpret_cast<const uint4*>(x0 + col + 8 * j));
-          if constexpr (TWO) xb[j] = __ldg(reinterpret_cast<const uint4*>(x1 + col + 8 * j));
-        }
-      }
+      uint4 xv[TWO ? 2 : 1][8];
+      few_load_x<TWO ? 2 : 1>(p, quad, stage, xv);
+      const uint4(&xa)[8] = xv[0];
+      const uint4(&xb)[8] = xv[TWO ? 1 : 0];
       const int stop = min(i1, i + nt - tile);
       float* out = sums + (tile * quads + quad) * kSlot + g * kRows + 2 * c;
       for (; i < stop; ++i, out += quads * kSlot) {
