@@ -344,6 +344,7 @@ __global__ void __launch_bounds__(32 * kColumnWarps) column_sum_bf16_kernel(cons
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t k = (int64_t)blockIdx.x * 32 + lane;
   float s = 0.0f;
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the parts come from the grid before
   if (k < n) {
 #pragma unroll 8
     for (int p = warp; p < parts; p += kColumnWarps) s += partial[(int64_t)p * n + k];
@@ -359,8 +360,16 @@ __global__ void __launch_bounds__(32 * kColumnWarps) column_sum_bf16_kernel(cons
 }
 
 static cudaError_t launch_column_sum(const float* partial, int parts, int64_t n, uint16_t* out, cudaStream_t st) {
-  column_sum_bf16_kernel<<<(unsigned)((n + 31) / 32), 32 * kColumnWarps, 0, st>>>(partial, parts, n, out);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((n + 31) / 32));
+  cfg.blockDim = dim3(32 * kColumnWarps);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, column_sum_bf16_kernel, partial, parts, n, out);
 }
 
 // Threads for `units` row units of 8 values, `vpt` per thread.
