@@ -180,8 +180,9 @@ struct NormBwdArgs {
   float* partial;         // [gridDim.x][K] sums of dy * n, or NULL
 };
 
-// Block b takes the tokens b, b + gridDim.x, ...; a thread owns up to VPT units of 8 features, the
-// same ones for every token, so the weight's gradient accumulates in its registers and leaves as
+// A block takes a run of tokens (every gridDim.x-th token instead read the same bytes 10 to 25 % slower:
+// 64.6 against 58.6 us for 8192 x 5120 with both optional parts); a thread owns up to VPT units of 8
+// features, the same ones for every token, so the weight's gradient accumulates in its registers and leaves as
 // one row of partial sums per block.  The rows of dy, h and dh of the next S - 1 tokens are on their
 // way into shared memory meanwhile: a thread copies and reads only its own units, so the ring
 // needs no barrier, and a token costs one barrier, that of its sum.
@@ -196,8 +197,8 @@ __global__ void __maxnreg__(VPT <= 2 ? 96 : 128) rmsnorm_bwd_kernel(const NormBw
   const float inv_k = 1.0f / (float)a.K;
   uint4* mine = ring + threadIdx.x;
   auto slot = [&](int stage, int row, int i) { return mine + ((stage * kRows + row) * VPT + i) * T; };
-  auto load = [&](int64_t m, int stage) {
-    if (m < a.M) {
+  auto load = [&](int64_t m, int stage, int64_t end) {
+    if (m < end) {
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
         const int c = i * T + threadIdx.x;
@@ -210,8 +211,10 @@ __global__ void __maxnreg__(VPT <= 2 ? 96 : 128) rmsnorm_bwd_kernel(const NormBw
     }
     cp_async_commit();
   };
+  const int64_t per = a.M / gridDim.x, extra = a.M - per * gridDim.x;
+  const int64_t first = blockIdx.x * per + min((int64_t)blockIdx.x, extra), last = first + per + (blockIdx.x < extra ? 1 : 0);
 #pragma unroll
-  for (int s = 0; s < S; ++s) load((int64_t)blockIdx.x + (int64_t)s * gridDim.x, s);
+  for (int s = 0; s < S; ++s) load(first + s, s, last);
   // pairs of fp32 values throughout: the paired instructions halve the arithmetic
   uint64_t w2[VPT][4], acc[DW ? VPT : 1][4];
 #pragma unroll
@@ -224,7 +227,7 @@ __global__ void __maxnreg__(VPT <= 2 ? 96 : 128) rmsnorm_bwd_kernel(const NormBw
     }
   }
   int stage = 0, flip = 0;
-  for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x) {
+  for (int64_t m = first; m < last; ++m) {
     const float rstd = __ldg(a.rstd + m);
     const uint64_t r2 = f32_pair(rstd, rstd);
     cp_async_wait<S - 1>();
@@ -269,7 +272,7 @@ __global__ void __maxnreg__(VPT <= 2 ? 96 : 128) rmsnorm_bwd_kernel(const NormBw
           make_uint4(pack_bf16x2(pair_lo(e[0]), pair_hi(e[0])), pack_bf16x2(pair_lo(e[1]), pair_hi(e[1])),
                      pack_bf16x2(pair_lo(e[2]), pair_hi(e[2])), pack_bf16x2(pair_lo(e[3]), pair_hi(e[3])));
     }
-    load(m + (int64_t)S * gridDim.x, stage);   // every value of this stage has been used
+    load(m + S, stage, last);   // every value of this stage has been used
     if (++stage == S) stage = 0;
   }
   if constexpr (DW) {
