@@ -77,6 +77,22 @@ def test_act8_is_bit_exact(M, K):
         assert a.nbytes() == codes.size + scales.size
 
 
+@pytest.mark.parametrize("M,K", [(64, 32), (16, 128), (1, 6144), (4, 13824), (2048, 96), (9480, 2048)])
+def test_act8_of_rows_of_whole_groups(M, K):
+    """Tensors that make one flat run of rows of 2048 are taken as such; sampled rows of the long one."""
+    x = _spread(M, K, M + 7 * K)
+    x[M // 2, K - 1] = float("nan")
+    a = q.act8_quantize(x.cuda())
+    back = q.act8_dequant(a)
+    rows = np.arange(M) if M < 4000 else np.r_[0:70, M // 2 - 70:M // 2 + 70, M - 70:M]
+    codes, scales = ob.act8_quantize(to_np64(x[rows]))
+    group = np.repeat(scales == 255, 32, axis=1)[:, :K]
+    assert group.any() and np.array_equal(a.scales.cpu().numpy()[rows], scales)
+    assert np.array_equal(a.codes.cpu().numpy()[rows][:, :K][~group], codes[:, :K][~group])
+    got = to_np64(back)[rows]
+    assert np.isnan(got[group]).all() and np.array_equal(got[~group], ob.act8_dequant(codes, scales, K)[~group])
+
+
 def test_act8_of_values_that_are_not_finite():
     x = _normal((4, 96), 1.0, 1)
     x[0, 3], x[1, 40], x[2, 95] = float("inf"), float("nan"), float("-inf")
@@ -306,6 +322,46 @@ def test_few_tokens_joined_in_a_block_and_from_a_flat_list(M, N, K, r):
     yr, zr, _ = _epi_ref(x, Wd, A, B, 0.5, bias, "silu", res)
     assert_within_tolerance(y, yr, "y")
     assert_within_tolerance(z, zr, "z")
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 2048, 512), (16, 2376, 3968), (5, 2376, 3968), (9, 2376, 2056)])
+def test_few_tokens_on_two_streams_and_in_graphs(M, N, K):
+    """Two calls at once, and two captured ones replayed on new tokens: what one call leaves in its
+    workspace is never another's."""
+    W = q.nf4_quantize_dq(_weight(N, K, 121).cuda())
+    inp = synth.linear_inputs(M, N, K, 16, 122)
+    A, B, x, res = inp["A"].cuda(), inp["B"].cuda(), inp["x"].cuda(), _normal((M, N), 2.0, 123).cuda()
+    other = torch.flip(x, dims=(1,)).contiguous()
+
+    def call(v):
+        return q.qlora_linear_epilogue_fwd(v, W, A, B, 0.5, activation="gelu", residual=res)[0]
+
+    want = [call(x).clone(), call(other).clone()]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for st in streams:
+        st.wait_stream(torch.cuda.current_stream())
+    outs = [[], []]
+    for _ in range(20):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                outs[i].append(call((x, other)[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(o, want[i]) for o in outs[i])
+    held = x.clone()
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            y = call(held)
+        graphs.append((g, y))
+    held.copy_(other)
+    for _ in range(3):
+        for g, _ in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    assert q.check_device_error() == 0
+    assert all(torch.equal(y, want[1]) for _, y in graphs)
 
 
 def test_linear_epilogue_identity_reproduces_the_weight():
