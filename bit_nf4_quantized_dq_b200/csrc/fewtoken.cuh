@@ -21,7 +21,7 @@
 //    more than an empty loop, at 36 MB.)  The 128-byte swizzle lets the lanes read them without bank
 //    conflicts.  The scales are one item ahead in registers.
 //  - tcgen05 would need the tile staged for 128 rows and at least 16 tokens; as 16-token tiles of the
-//    fused GEMM (with its K splits and a reduction) the same layer takes 52 us, here 22 us.
+//    fused GEMM (with its K splits and a reduction) the same layer takes 54 us, here 22 us.
 // With K % 64 != 0 code rows are only 4-byte aligned and blocks span rows: a kernel of its own reads
 // the codes into registers, in tiles of 8 rows.
 #pragma once
@@ -734,9 +734,9 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) few_token_ragged_kernel(con
 // How this path takes a shape.  Whole tiles join their sums in the block that owns them, where all of
 // a block's sums fit and the tiles load the SMs evenly.  Otherwise a flat list of the items over all
 // blocks loads them evenly and a second kernel joins, about 1 us more: with adapters and one token 22.8
-// against 22.2 us for 13824 x 5120 and 12.2 against 11.3 us for 4096 x 4096, but 25 against 33 us for
-// 5120 x 13824 (two or three tiles of 54 items per SM), and 42 against 51 us for 16 tokens of 13824 x
-// 5120, whose sums would take two rounds.
+// against 21.9 us for 13824 x 5120 and 11.4 against 10.1 us for 4096 x 4096, but 26.7 against 31.6 us for
+// 5120 x 13824 (two or three tiles of 54 items per SM), and 43 against 52 us for 16 tokens of 13824 x
+// 5120, whose sums would take two rounds; near the rule's 12 items they are equal (4096 x 11008: 18.0, 18.2).
 enum FewPlan : int { kFewNo = 0, kFewTiles = 1, kFewFlat = 2 };
 static FewPlan few_token_plan(int64_t M, int64_t K, int64_t N) {
   if (M > kFewTokens || N * K >= (1ll << 37)) return kFewNo;

