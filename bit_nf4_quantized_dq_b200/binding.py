@@ -374,15 +374,23 @@ def _require_weight(q: NF4Tensor, device) -> None:
     if len(q.shape) != 2:
         raise QNF4Error("the quantized weight must have two dimensions")
     nb = (q.numel + 63) // 64
-    parts = [(q.codes, torch.uint8, 32 * nb, "codes")]
+    _require_part(q.codes, torch.uint8, 32 * nb, device, "codes")
     if q.double_quant:
-        parts += [(q.scale_codes, torch.uint8, nb, "scale_codes"), (q.c2, torch.float32, (nb + 255) // 256, "c2"),
-                  (q.mean, torch.float32, 1, "mean")]
+        _require_part(q.scale_codes, torch.uint8, nb, device, "scale_codes")
+        _require_part(q.c2, torch.float32, (nb + 255) // 256, device, "c2")
+        _require_part(q.mean, torch.float32, 1, device, "mean")
     else:
-        parts += [(q.c2, torch.float32, nb, "scales")]
-    for t, dtype, count, name in parts:
-        if t is None or t.dtype != dtype or t.numel() < count or t.device != device or not t.is_contiguous():
-            raise QNF4Error(f"the weight's {name} must hold {count} contiguous {dtype} elements on {device}")
+        _require_part(q.c2, torch.float32, nb, device, "scales")
+
+
+def _require_part(t, dtype, count: int, device, name: str) -> None:
+    if t is None or t.dtype != dtype or t.numel() < count or t.device != device or not t.is_contiguous():
+        raise QNF4Error(f"the weight's {name} must hold {count} contiguous {dtype} elements on {device}")
+
+
+def _empty(rows: int, cols: int, dtype, device) -> torch.Tensor:
+    """A contiguous matrix (torch.empty takes 2.3 us of a call's 12 to 20 for the same)."""
+    return torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
 
 
 def _require_gpu(t: torch.Tensor, name: str) -> torch.device:
@@ -436,9 +444,8 @@ def _linear_bwd_act8(dY, x: Act8Tensor, t_saved, q: NF4Tensor, A, B, s: float, n
     _require(t_saved, torch.float32, (M, r), dev, "t_saved")
     _require(A, bf16, (r, K), dev, "A")
     _require(B, bf16, (N, r), dev, "B")
-    dX = torch.empty((M, K), dtype=bf16, device=dev) if need_dx else None
-    dA = torch.empty((r, K), dtype=bf16, device=dev)
-    dB = torch.empty((N, r), dtype=bf16, device=dev)
+    dX = _empty(M, K, bf16, dev) if need_dx else None
+    dA, dB = _empty(r, K, bf16, dev), _empty(N, r, bf16, dev)
     L = lib()
     ws = _workspace(workspace, L.qlora_linear_bwd_workspace_bytes(M, K, N, r), dev)
     cb, dq = q._format()

@@ -20,7 +20,7 @@ from typing import Optional, Union
 import torch
 
 from .binding import (
-    Act8Tensor, NF4Tensor, QNF4Error, _addr, _launch, _require, _require_act8, _require_gpu, _require_weight,
+    Act8Tensor, NF4Tensor, QNF4Error, _addr, _empty, _launch, _require, _require_act8, _require_gpu, _require_weight,
     _workspace, lib,
 )
 
@@ -42,8 +42,7 @@ def _matrix(t, name: str):
 
 
 def _empty_act8(M: int, K: int, dev) -> Act8Tensor:
-    return Act8Tensor(torch.empty((M, (K + 15) // 16 * 16), dtype=torch.uint8, device=dev),
-                      torch.empty((M, (K + 31) // 32), dtype=torch.uint8, device=dev), (M, K))
+    return Act8Tensor(_empty(M, (K + 15) // 16 * 16, torch.uint8, dev), _empty(M, (K + 31) // 32, torch.uint8, dev), (M, K))
 
 
 def act8_quantize(x: torch.Tensor) -> Act8Tensor:
@@ -60,7 +59,7 @@ def act8_dequant(a: Act8Tensor) -> torch.Tensor:
     dev = _require_gpu(a.codes, "a.codes")
     _require_act8(a, dev, "a")
     M, K = a.shape
-    out = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+    out = _empty(M, K, torch.bfloat16, dev)
     _launch(dev, "qnf4_act8_dequant", lib().qnf4_act8_dequant, a.codes.data_ptr(), a.scales.data_ptr(), M, K,
             out.data_ptr())
     return out
@@ -134,9 +133,9 @@ def qlora_linear_epilogue_fwd(x: torch.Tensor, q: NF4Tensor, A: Optional[torch.T
         _require(bias, bf16, (N,), dev, "bias")
     if residual is not None:
         _require(residual, bf16, (M, N), dev, "residual")
-    y = torch.empty((M, N), dtype=bf16, device=dev)
-    t = torch.empty((M, r), dtype=torch.float32, device=dev) if save and r else None
-    z = torch.empty((M, N), dtype=bf16, device=dev) if save and act else None
+    y = _empty(M, N, bf16, dev)
+    t = _empty(M, r, torch.float32, dev) if save and r else None
+    z = _empty(M, N, bf16, dev) if save and act else None
     L = lib()
     ws = _workspace(workspace, L.qlora_linear_epi_fwd_workspace_bytes(M, K, N, r), dev)
     cb, dq = q._format()
