@@ -330,7 +330,8 @@ int qlora_linear_bwd_act8(const uint16_t* dY, const uint8_t* x_codes, const uint
  * dh : bf16[M][K], the gradient that reaches h through the residual stream, or NULL for none.
  * The workspace is needed with dweight only: qlora_rmsnorm_bwd_workspace_bytes(M, K) bytes,
  * 256-byte aligned.
- * Sums are fp32.  Requirements: K % 8 == 0, eps finite and >= 0, bf16 operands and codes 16-byte
+ * Sums are fp32, that of the squares too: a row whose squares sum to more than 3.4e38 gets rstd = 0
+ * and y = 0 (NaN where v itself is not finite).  Requirements: K % 8 == 0, eps finite and >= 0, bf16 operands and codes 16-byte
  * aligned.  No output may overlap an input or another output.
  * ------------------------------------------------------------------------------------- */
 int qlora_rmsnorm_fwd(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int64_t M, int64_t K,
@@ -381,8 +382,8 @@ int qlora_epilogue_bwd(const uint16_t* dY, const uint16_t* z, const uint8_t* z_c
 
 /* ---------------------------------------------------------------------------------------
  * Launch plan of one forward / backward call of this shape (host-only, no device work):
- * the number of kernels each call enqueues, and the split factor of the K loop of the
- * fused dequant GEMMs (1 = no split).  Output pointers are HOST pointers and may be NULL.
+ * the number of kernels qlora_linear_fwd(_ex) and qlora_linear_bwd(_ex) enqueue, and the split
+ * factor of the K loop of the fused dequant GEMMs (1 = no split).  Output pointers are HOST pointers and may be NULL.
  * ------------------------------------------------------------------------------------- */
 int qlora_linear_plan(int64_t M, int64_t K, int64_t N, int r, int* fwd_launches, int* bwd_launches,
                       int* fwd_splits, int* dx_splits);

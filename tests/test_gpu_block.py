@@ -189,6 +189,14 @@ def test_rmsnorm_zero_rows_and_large_values():
     assert (q.act8_dequant(y8)[0] == 0).all()
 
 
+def test_rmsnorm_of_rows_whose_squares_overflow():
+    """The sum of the squares is fp32: past its range rstd and y are 0, NaN where v is not finite."""
+    x = torch.full((2, 64), 1e20, dtype=BF)
+    x[1, 5] = float("inf")
+    y, _, rstd, _ = q.rmsnorm_fwd(x.cuda(), torch.ones(64, dtype=BF, device="cuda"))
+    assert (rstd == 0).all() and (y[0] == 0).all() and torch.isnan(y[1, 5]) and (y[1, 6:] == 0).all()
+
+
 # --------------------------------------------------------- linear backward from a checkpoint
 def _weight(N, K, seed):
     return _normal((N, K), 0.02, seed)
