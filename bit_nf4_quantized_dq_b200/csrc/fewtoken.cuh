@@ -83,7 +83,7 @@ struct FewTokenDownParams {
 };
 
 template <int TOK>
-__global__ void __launch_bounds__(256) few_token_down_kernel(const FewTokenDownParams p) {
+__global__ void __maxnreg__(TOK == 1 ? 32 : 64) few_token_down_kernel(const FewTokenDownParams p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the product may start streaming W
   __shared__ float sums[8][TOK];
   const int j = blockIdx.x, m0 = blockIdx.y * TOK, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -287,8 +287,11 @@ __device__ __forceinline__ void few_finish(const FewTokenParams& p, const float*
 // K % 64 == 0.  TWO: more than 8 tokens.
 // FLAT: the blocks share one list of all items, columns outermost, whatever tile they cut; every item
 // leaves its sums in p.part for few_token_join_kernel.
+// Registers: 128 are what 16 warps can have.  With 112, and as much of the SM set aside for shared memory
+// by the down-projection, a block of that fits beside one of this: 24.4 instead of 26.5 us for one token
+// of 5120 x 13824 as a flat list; the tile form does not gain.
 template <bool TWO, bool FLAT>
-__global__ void __launch_bounds__(32 * kFewWarps, 1) few_token_kernel(const __grid_constant__ FewTokenParams p) {
+__global__ void __maxnreg__(TWO || !FLAT ? 128 : 112) few_token_kernel(const __grid_constant__ FewTokenParams p) {
   constexpr int kRows = 16, NT = TWO ? 2 : 1, kSlot = NT * kRows * 8;   // sums [group of 8 tokens][row][token]
   extern __shared__ __align__(16) uint8_t few_smem[];
   uint8_t* const smem0 = few_smem - smem_u32(few_smem);                // shared address 0
@@ -517,6 +520,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) few_token_kernel(const __gr
     if (p.t) {
       // t B^T: t as bf16 hi + lo (16 significant bits), one more slot of sums per tile
       asm volatile("griddepcontrol.wait;" ::: "memory");   // t comes from the grid before
+      constexpr int kSteps = TWO ? 2 : 4;
       const int first = FLAT ? (int)blockIdx.x * kFewWarps + warp : warp, step = FLAT ? (int)gridDim.x * kFewWarps : kFewWarps;
       for (int tl = first; tl < nt; tl += step) {
         const int64_t n0 = (int64_t)(t0 + tl) * kRows + g, n1 = min(n0 + 8, p.N - 1);
@@ -525,21 +529,36 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) few_token_kernel(const __gr
         for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int k = 0; k < 4; ++k) acc[t][k] = 0.0f;
-        for (int j = 4 * c; j < p.r + 4 * c; j += 16) {   // 16 rank columns a step: lane c takes 4 of them
-          uint2 b0 = make_uint2(0u, 0u), b1 = b0;
-          if (j < p.r) {
-            b0 = __ldg(reinterpret_cast<const uint2*>(p.B + n0 * p.r + j));
-            b1 = __ldg(reinterpret_cast<const uint2*>(p.B + n1 * p.r + j));
+        for (int j0 = 4 * c; j0 < p.r + 4 * c; j0 += 16 * kSteps) {
+          // 16 rank columns a step, lane c takes 4 of them; the loads of several steps go out together (one
+          // by one they took 1 us at rank 64)
+          uint2 b0[4], b1[kSteps];
+          float4 tv[NT][kSteps];
+#pragma unroll
+          for (int k = 0; k < kSteps; ++k) {
+            const int j = j0 + 16 * k;
+            b0[k] = b1[k] = make_uint2(0u, 0u);
+            if (j < p.r) {
+              b0[k] = __ldg(reinterpret_cast<const uint2*>(p.B + n0 * p.r + j));
+              b1[k] = __ldg(reinterpret_cast<const uint2*>(p.B + n1 * p.r + j));
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              tv[t][k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              if (j < p.r) tv[t][k] = *reinterpret_cast<const float4*>(p.t + (int64_t)min(8 * t + g, p.M - 1) * p.r + j);
+            }
           }
 #pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            float4 tv = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (j < p.r) tv = *reinterpret_cast<const float4*>(p.t + (int64_t)min(8 * t + g, p.M - 1) * p.r + j);
-            uint32_t h0, l0, h1, l1;
-            split_bf16x2(tv.x, tv.y, h0, l0);
-            split_bf16x2(tv.z, tv.w, h1, l1);
-            mma_bf16_16816(acc[t], b0.x, b1.x, b0.y, b1.y, h0, h1);
-            mma_bf16_16816(acc[t], b0.x, b1.x, b0.y, b1.y, l0, l1);
+          for (int k = 0; k < kSteps; ++k) {
+            if (j0 + 16 * k >= p.r + 4 * c) break;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              uint32_t h0, l0, h1, l1;
+              split_bf16x2(tv[t][k].x, tv[t][k].y, h0, l0);
+              split_bf16x2(tv[t][k].z, tv[t][k].w, h1, l1);
+              mma_bf16_16816(acc[t], b0[k].x, b1[k].x, b0[k].y, b1[k].y, h0, h1);
+              mma_bf16_16816(acc[t], b0[k].x, b1[k].x, b0[k].y, b1[k].y, l0, l1);
+            }
           }
         }
         float* out = sums + (nt * quads + tl) * kSlot + g * 8 + 2 * c;
@@ -734,7 +753,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) few_token_ragged_kernel(con
 // How this path takes a shape.  Whole tiles join their sums in the block that owns them, where all of
 // a block's sums fit and the tiles load the SMs evenly.  Otherwise a flat list of the items over all
 // blocks loads them evenly and a second kernel joins, about 1 us more: with adapters and one token 22.8
-// against 21.9 us for 13824 x 5120 and 11.4 against 10.1 us for 4096 x 4096, but 26.7 against 31.6 us for
+// against 21.8 us for 13824 x 5120 and 11 against 9.7 us for 4096 x 4096, but 24.4 against 31.6 us for
 // 5120 x 13824 (two or three tiles of 54 items per SM), and 43 against 52 us for 16 tokens of 13824 x
 // 5120, whose sums would take two rounds; near the rule's 12 items they are equal (4096 x 11008: 18.0, 18.2).
 enum FewPlan : int { kFewNo = 0, kFewTiles = 1, kFewFlat = 2 };
@@ -791,7 +810,27 @@ static cudaError_t launch_few_token(const FewTokenParams& p, FewPlan plan, cudaS
   return cudaLaunchKernelEx(&cfg, few_token_join_kernel, p, (int)quads + (p.t ? 1 : 0));
 }
 
+// The small kernels beside the product run with its split of the SM's memory, whatever they use of it.
+static cudaError_t few_same_split_once() {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  const uint64_t bit = (dev >= 0 && dev < 64) ? (1ull << dev) : 0ull;
+  if (e != cudaSuccess || (bit && (done.load(std::memory_order_acquire) & bit))) return e;
+  void (*down[2])(const FewTokenDownParams) = {few_token_down_kernel<1>, few_token_down_kernel<kFewDownTokens>};
+  for (auto* k : down)
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(few_token_join_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared);
+  if (e == cudaSuccess && bit) done.fetch_or(bit, std::memory_order_acq_rel);
+  return e;
+}
+
 static cudaError_t launch_few_token_down(const FewTokenDownParams& p, cudaStream_t st) {
+  cudaError_t e = few_same_split_once();
+  if (e != cudaSuccess) return e;
   if (p.M == 1) few_token_down_kernel<1><<<p.r, 256, 0, st>>>(p);
   else few_token_down_kernel<kFewDownTokens><<<dim3(p.r, (p.M + kFewDownTokens - 1) / kFewDownTokens), 256, 0, st>>>(p);
   return cudaGetLastError();
