@@ -14,6 +14,10 @@
 // A group with an infinity or a NaN has the scale byte 255 and decodes to NaN as a whole, so that
 // a diverged step does not look like a large finite one.
 //
+// Decoding takes any code and scale byte (a checkpoint may come from elsewhere): E4M3(code) *
+// 2^(byte - 127), NaN for the codes 0x7F and 0xFF and for the byte 255.  Bytes outside [10, 247], which
+// the quantizer does not write, give values that bf16 may have to round to a subnormal or infinity.
+//
 // Stored: codes uint8 [M][ld], ld = K rounded up to 16 (so that tile loads keep their 16-byte
 // row pitch; the pad holds zero codes); scales uint8 [M][ceil(K / 32)], byte e + 127.
 // 8.25 bits per value instead of 16.
@@ -80,9 +84,9 @@ __device__ __forceinline__ uint32_t a8_scale_byte(uint32_t amax_bits) {
 }
 // 2^-e of a scale byte: exponent field 127 - e = 254 - byte, in [7, 244].
 __device__ __forceinline__ float a8_inv_scale(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
-// 2^e of a scale byte; NaN for the byte 255.
+// 2^e of a scale byte (2^-127, subnormal, of the byte 0); NaN for the byte 255.
 __device__ __forceinline__ float a8_scale(uint32_t byte) {
-  return __uint_as_float(byte == kA8NanScale ? 0x7FC00000u : byte << 23);
+  return __uint_as_float(byte == kA8NanScale ? 0x7FC00000u : max(byte << 23, 0x00400000u));
 }
 
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
@@ -134,20 +138,24 @@ __device__ __forceinline__ float2 a8_decode2(uint32_t pair, float scale) {
 // per two values.  A code's exponent and mantissa bits (eeee mmm), moved to the low end of a
 // bf16's exponent and the top of its mantissa, read as the code's value times 2^-120 (the
 // exponent biases differ by 120; subnormal codes become subnormal bf16 values of the same ratio),
-// so one exact product with 2^(120 + e) restores it.  Scales above 2^7 would overflow that factor
-// and take a second product.
+// so one product with 2^(120 + e) restores it, exact for every scale that the quantizer writes.
+// Scales above 2^7 would overflow that factor and take a second product.  The NaN codes 0x7F and
+// 0xFF read as 480: a carry into their top bit finds them, and the call returns whether there are any, for
+// the caller to mark (a branch in here, between the units of a caller, cost dA 6 % of its time).
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-__device__ __forceinline__ void a8_decode16(const uint4& q, uint32_t byte, uint32_t (&o)[8]) {
+__device__ __forceinline__ uint32_t a8_decode16(const uint4& q, uint32_t byte, uint32_t (&o)[8]) {
   const uint32_t w[4] = {q.x, q.y, q.z, q.w};
   const int e = (int)byte - 127;
   const uint32_t f = byte == kA8NanScale ? 0x7FC0u : (uint32_t)(247 + min(e, 7)) << 7;
   const uint32_t f2 = f | (f << 16);
+  uint32_t nan = 0u;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
+    nan |= (w[i] & 0x7F7F7F7Fu) + 0x01010101u;
     const uint32_t a = prmt(w[i], 0u, 0x1404u), b = prmt(w[i], 0u, 0x3424u);
     o[2 * i] = mul_bf16x2((a & 0x80008000u) | ((a >> 4) & 0x07F007F0u), f2);
     o[2 * i + 1] = mul_bf16x2((b & 0x80008000u) | ((b >> 4) & 0x07F007F0u), f2);
@@ -156,6 +164,18 @@ __device__ __forceinline__ void a8_decode16(const uint4& q, uint32_t byte, uint3
     const uint32_t g = (uint32_t)(127 + e - 7) << 7, g2 = g | (g << 16);
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[i] = mul_bf16x2(o[i], g2);
+  }
+  return nan & 0x80808080u;
+}
+// NaN in the places of the NaN codes of q.
+__device__ __forceinline__ void a8_mark_nan16(const uint4& q, uint32_t (&o)[8]) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t m = ((w[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+    const uint32_t a = prmt(m, 0u, 0x1404u), b = prmt(m, 0u, 0x3424u);   // 0x8000 per NaN code
+    o[2 * i] |= a - (a >> 9);                                            // 0x7FC0
+    o[2 * i + 1] |= b - (b >> 9);
   }
 }
 

@@ -298,15 +298,23 @@ __device__ __forceinline__ void lowrank_block(const LowRankParams& p, int tile_r
       for (int i = 0; i < 4; ++i) cur[i] = byte[i];
       if (it + 1 < n_iters) fetch(it + 1);   // one k-block ahead
       if (!mbar_wait(&full[s], ph, abort_word, kErrWaitTma)) break;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      auto decode = [&](int i, bool mark) {
         const uint4 q = *reinterpret_cast<const uint4*>(codes + tok[i] * 128 + pc[i] * 16);
         uint32_t o[8];
-        a8_decode16(q, cur[i], o);
+        const uint32_t nan = a8_decode16(q, cur[i], o);
+        if (mark) a8_mark_nan16(q, o);
         uint8_t* row = A + (pc[i] >> 2) * 8192 + tok[i] * 128;
         const int j = 2 * (pc[i] & 3);
         *reinterpret_cast<uint4*>(row + ((j ^ (tok[i] & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
         *reinterpret_cast<uint4*>(row + (((j + 1) ^ (tok[i] & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+        return nan;
+      };
+      uint32_t nan = 0u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) nan |= decode(i, false);
+      if (nan) {   // NaN codes in a finite group, which only a checkpoint from elsewhere holds
+#pragma unroll
+        for (int i = 0; i < 4; ++i) decode(i, true);
       }
       fence_proxy_async_smem();
       __syncwarp();

@@ -292,7 +292,9 @@ int qlora_adamw_step(float* param, const uint16_t* grad, float* m, float* v, uin
  *   codes  : uint8 [M][ld], ld = K rounded up to 16, 16-byte aligned; the ld - K codes behind a
  *            row are 0
  *   scales : uint8 [M][ceil(K / 32)], scale byte b
- *   value  = E4M3(code) * 2^(b - 127), exact in bf16; every value of a group with b = 255 is NaN
+ *   value  = E4M3(code) * 2^(b - 127); NaN for the codes 0x7F and 0xFF and for every code of a group
+ *            with b = 255.  Exact in bf16 for b in [10, 247], all that the quantizer writes; with
+ *            other b rounded to nearest even there (a subnormal, or an infinity past the range)
  *
  * qnf4_act8_quantize: with amax the largest magnitude of a group, b - 127 is the smallest integer
  *   e with amax <= 448 * 2^e, clamped to [-117, 120]; code = E4M3 round-to-nearest-even of
