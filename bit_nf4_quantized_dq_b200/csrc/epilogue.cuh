@@ -10,6 +10,8 @@
 //   gelu_tanh  z p(2 u),     u = sqrt(2 / pi) (z + 0.044715 z^3)  slope p + z p (1 - p) 2 u'
 // The tanh form uses (1 + tanh u) / 2 = 1 / (1 + e^-2u), and the erf form erfc: neither loses its
 // small results for negative z to a cancellation against 1.
+// Slopes at an infinite z (what bf16 makes of a saved z above 3.39e38, too) are their limits, 0 or 1:
+// the term z p (1 - p) would be infinity times 0.  Values there are the formulas': act(-inf) is NaN but for ReLU.
 #pragma once
 
 #include "gemm.h"
@@ -78,6 +80,13 @@ __device__ __forceinline__ uint64_t act_value2(uint64_t z) {
   return z;
 }
 
+// The nearest finite value (of a NaN any: it meets the NaN of its logistic)
+__device__ __forceinline__ float nearest_finite(float v) {
+  float r;
+  asm("min.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(v), "f"(3.402823466e38f));   // the smaller magnitude, v's sign
+  return r;
+}
+
 // dy * act'(z) for two values at a time
 template <int ACT>
 __device__ __forceinline__ uint64_t act_grad2(uint64_t dy, uint64_t z) {
@@ -85,8 +94,8 @@ __device__ __forceinline__ uint64_t act_grad2(uint64_t dy, uint64_t z) {
   if constexpr (ACT == kActRelu) return f32_pair(z0 <= 0.0f ? 0.0f : pair_lo(dy), z1 <= 0.0f ? 0.0f : pair_hi(dy));
   const uint64_t one = f32_pair(1.0f, 1.0f), minus = f32_pair(-1.0f, -1.0f);
   if constexpr (ACT == kActSilu) {
-    const uint64_t p = f32_pair(logistic_ftz(z0), logistic_ftz(z1));
-    return f32x2_mul(dy, f32x2_fma(f32x2_mul(z, p), f32x2_fma(p, minus, one), p));
+    const uint64_t p = f32_pair(logistic_ftz(z0), logistic_ftz(z1)), v = f32_pair(nearest_finite(z0), nearest_finite(z1));
+    return f32x2_mul(dy, f32x2_fma(f32x2_mul(v, p), f32x2_fma(p, minus, one), p));
   }
   if constexpr (ACT == kActGelu) {
     // Abramowitz & Stegun 7.1.26: erfc(x) = t (a1 + t (a2 + ...)) e^-x^2 with t = 1 / (1 + p x), x >= 0,
@@ -122,9 +131,10 @@ __device__ __forceinline__ uint64_t act_grad2(uint64_t dy, uint64_t z) {
     const uint64_t v = f32x2_mul(z, f32x2_fma(zz, c1, cc)), slope = f32x2_fma(zz, c3, cc);
     const uint64_t p = f32_pair(logistic_ftz(pair_lo(v)), logistic_ftz(pair_hi(v)));
     const uint64_t q = f32x2_mul(f32x2_mul(z, p), f32x2_fma(p, minus, one));
-    // q is 0 where p has saturated; the slope of u may have overflowed there
-    const float t0 = pair_lo(q) == 0.0f ? 0.0f : pair_lo(q) * pair_lo(slope);
-    const float t1 = pair_hi(q) == 0.0f ? 0.0f : pair_hi(q) * pair_hi(slope);
+    // p has saturated long before the slope of u overflows; q is 0 there, or infinity times 0
+    const float inf = __uint_as_float(0x7F800000u);
+    const float t0 = pair_lo(slope) == inf ? 0.0f : pair_lo(q) * pair_lo(slope);
+    const float t1 = pair_hi(slope) == inf ? 0.0f : pair_hi(q) * pair_hi(slope);
     return f32x2_mul(dy, f32_pair(pair_lo(p) + t0, pair_hi(p) + t1));
   }
   return dy;

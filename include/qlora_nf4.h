@@ -362,6 +362,8 @@ int qlora_rmsnorm_bwd(const uint16_t* dy, const uint16_t* dh, const uint16_t* h,
  * qlora_epilogue_bwd: dZ = dY * act'(z) (bf16[M][N]) and dbias = sum over tokens of dZ before its
  * rounding (bf16[N], or NULL), for z as saved or as an 8-bit checkpoint of it (z_codes, z_scales;
  * z is then NULL).  qlora_linear_bwd takes dZ for its dY; the residual's gradient is dY itself.
+ * At an infinite z the slope act' is its limit, 0 or 1 (act itself is as the formulas give it: NaN at
+ * -infinity, but for ReLU).
  * With QNF4_ACT_NONE dZ is dY: z and dZ are NULL and only dbias is computed.  The workspace is
  * needed with dbias only: qlora_epilogue_bwd_workspace_bytes(M, N) bytes, 256-byte aligned.
  * Requirements: N % 8 == 0; dY, z, z_codes and dZ 16-byte aligned.

@@ -51,3 +51,48 @@ def test_act8_decoders_agree_on_every_code_and_scale_byte(first):
     want = q.qlora_linear_bwd(dY, d, t, W, A, B, 0.5)
     assert torch.equal(dX, want[0]) and _same(dA, want[1]) and torch.equal(dB, want[2])
     assert torch.isnan(dA[:, 127]).all() and torch.isnan(dA[:, 255]).all()
+
+
+# ------------------------------------------------------------------------------- activations
+INF = float("inf")
+
+
+@pytest.mark.parametrize("act", ob.ACTIVATIONS[1:])
+def test_epilogue_bwd_at_infinite_pre_activations(act):
+    """The slopes' limits, 0 and 1, with a gradient of zero too; a NaN stays one (ReLU's slope at a NaN passes
+    the gradient)."""
+    z = torch.tensor([-INF, INF, -3.38e38, 3.38e38, -INF, INF, float("nan"), 0.0], dtype=BF).repeat(3, 1)
+    dy = torch.tensor([2.0, 2.0, 2.0, 2.0, 0.0, 0.0, 1.0, 0.0], dtype=BF).repeat(3, 1)
+    dz, db = q.epilogue_bwd(dy.cuda(), z.cuda(), act, need_dbias=True)
+    want = torch.tensor([0.0, 2.0, 0.0, 2.0, 0.0, 0.0, 1.0 if act == "relu" else float("nan"), 0.0]).repeat(3, 1)
+    assert _same(dz.float().cpu(), want) and _same(db.float().cpu(), want.sum(dim=0))
+
+
+@pytest.mark.parametrize("M", [400, 16, 8, 1])
+@pytest.mark.parametrize("act", ob.ACTIVATIONS[1:])
+def test_activations_over_their_whole_range(act, M):
+    """Every pre-activation from -30 to 30 through a layer of one weight, in calls of M tokens, and infinite
+    ones through the bias: the formulas' own values, infinite, NaN at -infinity but for ReLU."""
+    N, K = 8, 64
+    Wm = torch.zeros((N, K), dtype=BF)
+    Wm[:, 0] = 1.0
+    W = q.nf4_quantize_dq(Wm.cuda())
+    assert (q.nf4_dequant(W)[:, 0] == 1).all()
+    v = torch.linspace(-30, 30, 400).to(BF)
+    x = torch.zeros((400, K), dtype=BF)
+    x[:, 0] = v
+    x = x.cuda()
+    out = torch.cat([q.qlora_linear_epilogue_fwd(x[i:i + M], W, None, None, 1.0, activation=act)[0] for i in range(0, 400, M)])
+    zz = np.abs(to_np64(v))[:, None]
+    ref = ob.act(to_np64(v)[:, None] * np.ones(N), act)
+    # the exponent's argument v = 2 u, rounded, with |v| <= 2 |z| (1 + z^2); below 2^-126 the reciprocal is
+    # flushed, so z p is off by |z| 2^-126 at most, and a bf16 result by 2^-134
+    bound = (H + (8 + 2 * zz * (1 + zz * zz)) * 2.0 ** -23) * np.abs(ref) + zz * 2.0 ** -126 + 2.0 ** -130
+    assert (np.abs(to_np64(out) - ref) <= bound).all()
+    ends = torch.tensor([-INF, INF, 0.0, float("nan"), -INF, INF, 1e38, -1e38], dtype=BF)
+    y, _, z = q.qlora_linear_epilogue_fwd(torch.zeros((M, K), dtype=BF, device="cuda"), W, None, None, 1.0, bias=ends.cuda(),
+                                          activation=act, save=True)
+    assert _same(z.cpu(), ends.repeat(M, 1))
+    low = 0.0 if act == "relu" else float("nan")
+    want = torch.tensor([low, INF, 0.0, float("nan"), low, INF, 1e38, 0.0]).to(BF).repeat(M, 1)
+    assert _same(y.cpu(), want)
