@@ -387,11 +387,11 @@ constexpr int kDqWarps = kDqThreads / 32;
 constexpr int kDqChunk = 8 * kDqThreads;       // group sums per pass
 constexpr int kMaxMeanChunks = 1024;           // 2^23 groups: numel up to 2^37
 
-__global__ void __launch_bounds__(kDqThreads, 1) dq_mean_groups_kernel(const float* __restrict__ absmax,
-                                                                    const double* __restrict__ gsum, int64_t nb,
-                                                                    int64_t ng, float* __restrict__ mean_out,
-                                                                    uint8_t* __restrict__ scale_codes,
-                                                                    float* __restrict__ c2, int sw_encode) {
+// (No __restrict__: the quantize grid may still write `absmax` and `gsum` when this one starts, and a promise
+// of unchanging memory would let their loads move in front of the wait.)
+__global__ void __launch_bounds__(kDqThreads, 1) dq_mean_groups_kernel(const float* absmax, const double* gsum, int64_t nb,
+                                                                    int64_t ng, float* mean_out, uint8_t* scale_codes,
+                                                                    float* c2, int sw_encode) {
   __shared__ double warp_sum[kDqWarps];
   __shared__ double chunk_sum[kMaxMeanChunks];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

@@ -342,8 +342,10 @@ __global__ void __launch_bounds__(512) rmsnorm_bwd_long_kernel(const NormBwdArgs
 // 8 warps the 1480 parts of a 560-wide norm took 8 us, three quarters of its gradient's time.)
 constexpr int kColumnWarps = 32;
 
-__global__ void __launch_bounds__(32 * kColumnWarps) column_sum_bf16_kernel(const float* __restrict__ partial, int parts,
-                                                                            int64_t n, uint16_t* __restrict__ out) {
+// (`partial` is not __restrict__: the grid before may still write it when this one starts, and a promise of
+// unchanging memory would let its loads move in front of the wait.)
+__global__ void __launch_bounds__(32 * kColumnWarps) column_sum_bf16_kernel(const float* partial, int parts, int64_t n,
+                                                                            uint16_t* out) {
   __shared__ float sums[kColumnWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t k = (int64_t)blockIdx.x * 32 + lane;
