@@ -11,7 +11,7 @@ import torch
 import bit_nf4_quantized_dq_b200 as q
 import synth
 from oracle import block as ob
-from parity_util import to_np64
+from parity_util import assert_within_tolerance, to_np64
 
 pytestmark = pytest.mark.gpu
 
@@ -96,3 +96,51 @@ def test_activations_over_their_whole_range(act, M):
     low = 0.0 if act == "relu" else float("nan")
     want = torch.tensor([low, INF, 0.0, float("nan"), low, INF, 1e38, 0.0]).to(BF).repeat(M, 1)
     assert _same(y.cpu(), want)
+
+
+# ------------------------------------------------------------- rarer routes of a few tokens
+def _against_float64(M, N, K, r, act, seed):
+    """A call with everything in its epilogue, all outputs against float64 on the dequantized weight (bit-exact
+    against the oracle elsewhere); x is scaled so that the products' fp32 sums stay far inside the tolerance's
+    floor of 2e-4 (thousands of terms of 2^-4 * 0.02, each addition off by 2^-24 of a sum below 1)."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+
+    def normal(shape, std):
+        return (torch.randn(shape, generator=g, device="cuda") * std).to(BF)
+
+    W = q.nf4_quantize_dq(normal((N, K), 0.02))
+    A, B = (normal((r, K), r ** -0.5), normal((N, r), 0.02)) if r else (None, None)
+    x, bias, res = normal((M, K), 2.0 ** -4), normal((N,), 0.5), normal((M, N), 2.0)
+
+    def call():
+        return q.qlora_linear_epilogue_fwd(x, W, A, B, 0.5, bias=bias, activation=act, residual=res, save=True)
+
+    y, t, z = call()
+    again = call()
+    torch.cuda.synchronize()
+    assert q.check_device_error() == 0 and torch.equal(again[0], y) and torch.equal(again[2], z)
+    zr = x.double() @ q.nf4_dequant(W).double().T + bias.double()
+    if r:
+        tr = 0.5 * (x.double() @ A.double().T)
+        zr += tr @ B.double().T
+        mag = 0.5 * (x.double().abs() @ A.double().abs().T)
+        assert ((t.double() - tr).abs() <= 128 * 2.0 ** -23 * mag).all()
+    zr = zr.cpu().numpy()
+    assert_within_tolerance(z, zr, "z")
+    assert_within_tolerance(y, ob.act(zr, act) + to_np64(res), "y")
+
+
+@pytest.mark.parametrize("M,N,K,r", [(1, 5120, 13816, 64), (16, 5120, 13816, 64), (16, 13824, 5112, 8), (9, 13824, 5112, 0),
+                                     (8, 5120, 13816, 0)])
+def test_ragged_layers_whose_sums_take_several_rounds(M, N, K, r):
+    """K % 64 != 0 and more row tiles per SM than the sums of a block have room for: two rounds of tiles (the
+    first, third, fourth and last shape), three (the second)."""
+    _against_float64(M, N, K, r, "silu", 211)
+
+
+@pytest.mark.parametrize("M,N,K,r", [(9, 18944, 32008, 16), (16, 18952, 32008, 0), (11, 520, 32008, 16), (5, 136, 64264, 8)])
+def test_few_tokens_of_rows_too_long_for_the_few_token_path(M, N, K, r):
+    """K % 64 != 0 and rows whose sums do not fit: 16-token tiles, with their epilogue in the tiles where
+    N fills the SMs, behind a K split otherwise."""
+    _against_float64(M, N, K, r, "gelu", 212)
