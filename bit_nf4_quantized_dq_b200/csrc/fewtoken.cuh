@@ -756,6 +756,13 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) few_token_ragged_kernel(con
 // against 21.8 us for 13824 x 5120 and 11 against 9.7 us for 4096 x 4096, but 24.4 against 31.6 us for
 // 5120 x 13824 (two or three tiles of 54 items per SM), and 43 against 52 us for 16 tokens of 13824 x
 // 5120, whose sums would take two rounds; near the rule's 12 items they are equal (4096 x 11008: 18.0, 18.2).
+// With K % 64 != 0 the other side is 16-token tiles of the fused GEMM with the same epilogue (SiLU, residual, rank
+// 64): 1 token 26.6 against 85 us for 13824 x 5112, 11.2 against 31 for 4000 x 3000, 18 against 43 for 128 x
+// 30008; 16 tokens 45.5 against 85, 16.8 against 31 and 39 against 42.  Rows of thousands of columns in two and more
+// rounds come near at 16 tokens (70 against 90 us for 5120 x 13816, 99.4 against 99.8 for 4096 x 20008) and lose 2
+// to 6 % at the longest (144 against 141 for 4096 x 30008, 270 against 256 for 13824 x 18008).  Without adapters the
+// tiles need two launches less: 59.8 against 77 us for 5120 x 13816, but 32.9 against 26.9 for 128 x 30008.  A bound on
+// K would give away more at 9 tokens (66 against 84 us for 2048 x 30008) than it gains there.
 enum FewPlan : int { kFewNo = 0, kFewTiles = 1, kFewFlat = 2 };
 static FewPlan few_token_plan(int64_t M, int64_t K, int64_t N) {
   if (M > kFewTokens || N * K >= (1ll << 37)) return kFewNo;
