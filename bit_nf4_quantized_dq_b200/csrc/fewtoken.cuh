@@ -36,6 +36,7 @@ namespace qnf4 {
 constexpr int kFewTokens = 16;    // most tokens of this path
 constexpr int kFewCols = 256;     // columns per work item
 constexpr int kFewWarps = 16;
+constexpr int kFewBlocks = 148;   // one per SM
 // Shared memory.  The table sits at shared address 65536, so that its address bytes are (lane * 8, code
 // byte, 1, 0): one permute of the codes and a lane constant.  The items' sums lie in front of it, from
 // the start of the block's part on, the warps' rings of codes behind it.
@@ -48,9 +49,8 @@ static_assert(kFewSmemBytes <= 227 * 1024, "shared memory of one block");
 constexpr int kFewStageBytes = 4 * kFewCols * 2;   // x of four tokens
 constexpr int kFewRaggedSmemBytes = (int)kFewRingAddr + kFewWarps * kFewStageBytes;
 static_assert(kFewStageBytes <= kFewItemBytes, "a slot of the ring hands over x");
-// Room for sums: the block's part of shared memory starts 1 KB up.  (The kernels measure it, and take
-// their tiles in more rounds if there is less.)
-constexpr int kFewSumBytes = 63 * 1024;
+// Room for sums: the block's part of shared memory starts 1 KB up (checked at the launch).
+constexpr int kFewReservedBytes = 1024, kFewSumBytes = (int)kFewTableAddr - kFewReservedBytes;
 
 struct FewTokenParams {
   CUtensorMap map;         // codes [N][K / 2], boxes of 16 rows x 128 bytes, 128-byte swizzle (K % 64 == 0)
@@ -200,23 +200,24 @@ __device__ __forceinline__ void few_expand8(uint32_t w, float scale, uint32_t la
   few_round8(q, f32_pair(scale, scale), o);
 }
 
-// A block's share of `tiles`, and its rounds of even sizes whose sums (`slot` floats per item, `quads`
-// items per tile and one more for the adapter term) fit between `sums` and the table.
+// A block's share of `tiles`.
 struct FewShare {
-  int begin, end, per_round;
+  int begin, end;
 };
-__device__ __forceinline__ FewShare few_share(const float* sums, int tiles, int quads, int slot) {
+__device__ __forceinline__ FewShare few_share(int tiles) {
   const int base = tiles / (int)gridDim.x, extra = tiles - base * (int)gridDim.x;
   FewShare s;
   s.begin = (int)blockIdx.x * base + min((int)blockIdx.x, extra);
   s.end = s.begin + base + ((int)blockIdx.x < extra ? 1 : 0);
-  s.per_round = s.end - s.begin;
-  const int room = (int)(kFewTableAddr - smem_u32(sums)), one = 4 * slot * (quads + 1);
-  if ((int64_t)s.per_round * one > room) {   // (the divisions are not free at the start of a short kernel)
-    const int most = room / one, rounds = (s.per_round + most - 1) / most;
-    s.per_round = (s.per_round + rounds - 1) / rounds;
-  }
   return s;
+}
+// The tiles of a round: rounds of even sizes whose sums (`slot` floats per item, `quads` items per tile and one more
+// for the adapter term) fit between the start of shared memory and the table.
+__device__ __forceinline__ int few_per_round(int tiles, int quads, int slot) {
+  const int one = 4 * slot * (quads + 1);
+  if ((int64_t)tiles * one <= kFewSumBytes) return tiles;   // (the divisions are not free at the start of a short kernel)
+  const int most = kFewSumBytes / one, rounds = (tiles + most - 1) / most;
+  return (tiles + rounds - 1) / rounds;
 }
 
 // This lane's 64 columns (64 c .. 64 c + 63 of the quad) of its tokens g and, with NT = 2, g + 8, zeros
@@ -311,9 +312,8 @@ __global__ void __maxnreg__(TWO || !FLAT ? 128 : 112) few_token_kernel(const __g
 
   const int quads = (int)((p.K + kFewCols - 1) / kFewCols);
   const int tiles = (int)((p.N + kRows - 1) / kRows);
-  const FewShare share = FLAT ? FewShare{0, tiles, tiles} : few_share(sums, tiles, quads, kSlot);
+  const FewShare share = FLAT ? FewShare{0, tiles} : few_share(tiles);
   const float mean = p.scale_fp32 ? 0.0f : __ldg(p.mean);
-  uint32_t lane_addr = 0u;
   int slot = 0, pending = 0;     // the ring's slot read next, and its loads on their way
   uint32_t phase = 0u;
   bool ok = true;
@@ -326,258 +326,252 @@ __global__ void __maxnreg__(TWO || !FLAT ? 128 : 112) few_token_kernel(const __g
       if (tok < p.M && n < p.N) p.part[((int64_t)at_quad * p.M + tok) * p.N + n] = v[k];
     }
   };
-  for (int t0 = share.begin; t0 < share.end; t0 += share.per_round) {
-    const int nt = min(share.end - t0, share.per_round);
-    const int items = nt * quads;
-    int i0 = items * warp / kFewWarps, i1 = items * (warp + 1) / kFewWarps;
-    if constexpr (FLAT) {
-      const int64_t parts = (int64_t)gridDim.x * kFewWarps, part = (int64_t)blockIdx.x * kFewWarps + warp;
-      i0 = (int)(items * part / parts);
-      i1 = (int)(items * (part + 1) / parts);
+  const int t0 = share.begin, nt = share.end - share.begin;   // with tiles, all of their sums fit (few_token_plan)
+  const int items = nt * quads;
+  int i0 = items * warp / kFewWarps, i1 = items * (warp + 1) / kFewWarps;
+  if constexpr (FLAT) {
+    const int64_t parts = (int64_t)gridDim.x * kFewWarps, part = (int64_t)blockIdx.x * kFewWarps + warp;
+    i0 = (int)(items * part / parts);
+    i1 = (int)(items * (part + 1) / parts);
+  }
+  int quad = i0 / nt, tile = i0 - quad * nt;
+  // the item whose codes are loaded next
+  int c_quad = quad, c_tile = tile, c_left = i1 - i0;
+  auto load_codes = [&](int s) {
+    if (c_left == 0) return;
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&full[s], kFewItemBytes);
+      tma_load_2d(ring + s * kFewItemBytes, &p.map, c_quad * (kFewCols / 2), (t0 + c_tile) * kRows, &full[s]);
     }
-    int quad = i0 / nt, tile = i0 - quad * nt;
-    // the item whose codes are loaded next
-    int c_quad = quad, c_tile = tile, c_left = i1 - i0;
-    auto load_codes = [&](int s) {
-      if (c_left == 0) return;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&full[s], kFewItemBytes);
-        tma_load_2d(ring + s * kFewItemBytes, &p.map, c_quad * (kFewCols / 2), (t0 + c_tile) * kRows, &full[s]);
+    --c_left;
+    ++pending;
+    if (++c_tile == nt) {
+      c_tile = 0;
+      ++c_quad;
+    }
+  };
+  // The first loads go out as one instruction of as many lanes (an instruction holds its thread for
+  // hundreds of cycles, whatever the number of its lanes).
+  {
+    const int ahead = min(kFewRing - 1, c_left);   // the last slot hands over x first
+    int my_quad = c_quad, my_tile = c_tile;
+    for (int k = 0; k < ahead; ++k) {
+      if (k == lane) {
+        my_quad = c_quad;
+        my_tile = c_tile;
       }
-      --c_left;
-      ++pending;
       if (++c_tile == nt) {
         c_tile = 0;
         ++c_quad;
       }
-    };
-    // The first loads go out as one instruction of as many lanes (an instruction holds its thread for
-    // hundreds of cycles, whatever the number of its lanes).
-    {
-      const int ahead = min(kFewRing - 1, c_left);   // the last slot hands over x first
-      const int to = slot + lane < kFewRing ? slot + lane : slot + lane - kFewRing;
-      int my_quad = c_quad, my_tile = c_tile;
-      for (int k = 0; k < ahead; ++k) {
-        if (k == lane) {
-          my_quad = c_quad;
-          my_tile = c_tile;
-        }
-        if (++c_tile == nt) {
-          c_tile = 0;
-          ++c_quad;
-        }
-      }
-      if (lane < ahead) {
-        mbar_arrive_expect_tx(&full[to], kFewItemBytes);
-        tma_load_2d(ring + to * kFewItemBytes, &p.map, my_quad * (kFewCols / 2), (t0 + my_tile) * kRows, &full[to]);
-      }
-      c_left -= ahead;
-      pending = ahead;
-      __syncwarp();
     }
-    // The scales of the next item.  Columns past K (whose codes arrive as zeros, and where x is zero) and
-    // rows past N (N is a multiple of 8; their sums are not used) take the scales before them.
-    int f_quad = quad, f_tile = tile;
-    uint32_t f_blk[2] = {0u, 0u};
-    auto place = [&]() {
-      const int64_t col = min((int64_t)f_quad * kFewCols + 64 * c, p.K - 64);
+    if (lane < ahead) {
+      mbar_arrive_expect_tx(&full[lane], kFewItemBytes);
+      tma_load_2d(ring + lane * kFewItemBytes, &p.map, my_quad * (kFewCols / 2), (t0 + my_tile) * kRows, &full[lane]);
+    }
+    c_left -= ahead;
+    pending = ahead;
+    __syncwarp();
+  }
+  // The scales of the next item.  Columns past K (whose codes arrive as zeros, and where x is zero) and
+  // rows past N (N is a multiple of 8; their sums are not used) take the scales before them.
+  int f_quad = quad, f_tile = tile;
+  uint32_t f_blk[2] = {0u, 0u};
+  auto place = [&]() {
+    const int64_t col = min((int64_t)f_quad * kFewCols + 64 * c, p.K - 64);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int64_t n = (int64_t)(t0 + f_tile) * kRows + g + 8 * h;
+      f_blk[h] = (uint32_t)((min(n, p.N - 1) * p.K + col) >> 6);
+    }
+  };
+  FewScale next[2];
+  auto fetch = [&]() {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) next[h] = few_scale(p, f_blk[h]);
+    ++f_tile;
+    if (f_tile == nt) {
+      f_tile = 0;
+      ++f_quad;
+    }
+    if (f_tile == 0 || f_tile == nt - 1) {   // (the last tile's second half may lie past N)
+      place();
+    } else {
+      f_blk[0] += (uint32_t)(p.K >> 2);      // 16 rows of K / 64 blocks
+      f_blk[1] += (uint32_t)(p.K >> 2);
+    }
+  };
+  if (i0 < i1) {
+    place();
+    fetch();
+  }
+  uint4 xv[NT][8];
+  // x by way of a free slot of the ring, which then takes its codes; with two groups of tokens each lane
+  // reads its own (their registers leave no room for rows on their way: 44.8 us instead of 42.8 for 16
+  // tokens of 13824 x 5120)
+  auto load_x = [&](int s) {
+    if constexpr (TWO) {
+      load_codes(s);
+      const int64_t col = (int64_t)quad * kFewCols + 64 * c;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {   // tokens past M repeat the last one, unread
+        const uint4* src = reinterpret_cast<const uint4*>(p.x + (int64_t)min(8 * t + g, p.M - 1) * p.K + col);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) xv[t][j] = col < p.K ? __ldg(src + j) : make_uint4(0u, 0u, 0u, 0u);
+      }
+    } else {
+      few_load_x<NT>(p, quad, ring + s * kFewItemBytes, xv);
+      fence_proxy_async_smem();
+      __syncwarp();
+      load_codes(s);
+    }
+  };
+  if (i0 < i1) load_x(kFewRing - 1);
+  const uint32_t lane_addr = few_fill_table(p, smem0 + kFewTableAddr);   // while the codes arrive
+  if constexpr (FLAT) {
+    const int64_t tile16 = (int64_t)blockIdx.x * kFewWarps;
+    few_prefetch_rows(p, min(tile16 * kRows, p.N), min((tile16 + kFewWarps) * kRows, p.N), false);
+  } else {
+    few_prefetch_rows(p, (int64_t)share.begin * kRows, min((int64_t)share.end * kRows, p.N), true);
+  }
+  for (int i = i0; i < i1 && ok;) {
+    // this warp's tiles of one quad of columns
+    const int stop = min(i1, i + nt - tile);
+    float* out = sums + (tile * quads + quad) * kSlot + g * 8 + 2 * c;
+    for (; i < stop; ++i, out += quads * kSlot) {
+      const FewScale s0 = next[0], s1 = next[1];
+      if (i + 1 < i1) fetch();
+      if (!mbar_try_wait(&full[slot], phase) && !mbar_wait_thread(&full[slot], phase, abort_word, kErrWaitTma)) ok = false;
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (!ok) break;
+      // rows g and g + 8: their 16-byte chunks 2 c and 2 c + 1 lie at (chunk ^ g), a phase of 8 lanes (two
+      // rows) reads 8 different bank groups
+      const uint8_t* row = ring + slot * kFewItemBytes + g * 128;
+      const float f0 = few_scale_value(p, s0, mean), f1 = few_scale_value(p, s1, mean);
+      float acc[NT][2][4];
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[t][0][k] = acc[t][1][k] = 0.0f;
+      uint4 qa[2], qb[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int64_t n = (int64_t)(t0 + f_tile) * kRows + g + 8 * h;
-        f_blk[h] = (uint32_t)((min(n, p.N - 1) * p.K + col) >> 6);
+        qa[h] = *reinterpret_cast<const uint4*>(row + (((2 * c + h) ^ g) << 4));
+        qb[h] = *reinterpret_cast<const uint4*>(row + 1024 + (((2 * c + h) ^ g) << 4));
       }
-    };
-    FewScale next[2];
-    auto fetch = [&]() {
+      const uint32_t wa[8] = {qa[0].x, qa[0].y, qa[0].z, qa[0].w, qa[1].x, qa[1].y, qa[1].z, qa[1].w};
+      const uint32_t wb[8] = {qb[0].x, qb[0].y, qb[0].z, qb[0].w, qb[1].x, qb[1].y, qb[1].z, qb[1].w};
+      const uint64_t v0 = f32_pair(f0, f0), v1 = f32_pair(f1, f1);
+      // the lookups of the next 8 columns are on their way while these are rounded and multiplied
+      uint64_t la[2][4], lb[2][4];
+      few_lookup8(wa[0], lane_addr, la[0]);
+      few_lookup8(wb[0], lane_addr, lb[0]);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) next[h] = few_scale(p, f_blk[h]);
-      ++f_tile;
-      if (f_tile == nt) {
-        f_tile = 0;
-        ++f_quad;
-      }
-      if (f_tile == 0 || f_tile == nt - 1) {   // (the last tile's second half may lie past N)
-        place();
-      } else {
-        f_blk[0] += (uint32_t)(p.K >> 2);      // 16 rows of K / 64 blocks
-        f_blk[1] += (uint32_t)(p.K >> 2);
-      }
-    };
-    if (i0 < i1) {
-      place();
-      fetch();
-    }
-    uint4 xv[NT][8];
-    // x by way of a free slot of the ring, which then takes its codes; with two groups of tokens each lane
-    // reads its own (their registers leave no room for rows on their way: 44.8 us instead of 42.8 for 16
-    // tokens of 13824 x 5120)
-    auto load_x = [&](int s) {
-      if constexpr (TWO) {
-        load_codes(s);
-        const int64_t col = (int64_t)quad * kFewCols + 64 * c;
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {   // tokens past M repeat the last one, unread
-          const uint4* src = reinterpret_cast<const uint4*>(p.x + (int64_t)min(8 * t + g, p.M - 1) * p.K + col);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) xv[t][j] = col < p.K ? __ldg(src + j) : make_uint4(0u, 0u, 0u, 0u);
+      for (int j = 0; j < 8; ++j) {
+        if (j < 7) {
+          few_lookup8(wa[j + 1], lane_addr, la[(j + 1) & 1]);
+          few_lookup8(wb[j + 1], lane_addr, lb[(j + 1) & 1]);
         }
-      } else {
-        few_load_x<NT>(p, quad, ring + s * kFewItemBytes, xv);
-        fence_proxy_async_smem();
-        __syncwarp();
-        load_codes(s);
+        uint32_t a[4], b[4];
+        few_round8(la[j & 1], v0, a);
+        few_round8(lb[j & 1], v1, b);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const uint4& x = xv[t][j];
+          mma_bf16_16816(acc[t][0], a[0], b[0], a[1], b[1], x.x, x.y);
+          mma_bf16_16816(acc[t][1], a[2], b[2], a[3], b[3], x.z, x.w);
+        }
       }
-    };
-    if (i0 < i1) load_x(slot == 0 ? kFewRing - 1 : slot - 1);
-    if (lane_addr == 0u) {   // while the codes arrive
-      lane_addr = few_fill_table(p, smem0 + kFewTableAddr);
-      if constexpr (FLAT) {
-        const int64_t tile16 = (int64_t)blockIdx.x * kFewWarps;
-        few_prefetch_rows(p, min(tile16 * kRows, p.N), min((tile16 + kFewWarps) * kRows, p.N), false);
-      } else {
-        few_prefetch_rows(p, (int64_t)share.begin * kRows, min((int64_t)share.end * kRows, p.N), true);
+      --pending;
+      __syncwarp();   // every lane has used its codes: the slot takes the item kFewRing ahead
+      const int used = slot;
+      const bool turn = i + 1 == stop && stop < i1;   // to the next quad of columns
+      if (!turn) load_codes(used);
+      if (++slot == kFewRing) {
+        slot = 0;
+        phase ^= 1u;
+      }
+      // sums of rows g and g + 8, tokens 2 c and 2 c + 1 of each group
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        if constexpr (FLAT) {
+          const float both[4] = {acc[t][0][0] + acc[t][1][0], acc[t][0][1] + acc[t][1][1],
+                                 acc[t][0][2] + acc[t][1][2], acc[t][0][3] + acc[t][1][3]};
+          store_flat(quad, tile, t, both);
+        } else {
+          *reinterpret_cast<float2*>(out + t * 128) =
+              make_float2(acc[t][0][0] + acc[t][1][0], acc[t][0][1] + acc[t][1][1]);
+          *reinterpret_cast<float2*>(out + t * 128 + 64) =
+              make_float2(acc[t][0][2] + acc[t][1][2], acc[t][0][3] + acc[t][1][3]);
+        }
+      }
+      if constexpr (FLAT) ++tile;
+      if (turn) {
+        ++quad;
+        load_x(used);
       }
     }
-    for (int i = i0; i < i1 && ok;) {
-      // this warp's tiles of one quad of columns
-      const int stop = min(i1, i + nt - tile);
-      float* out = sums + (tile * quads + quad) * kSlot + g * 8 + 2 * c;
-      for (; i < stop; ++i, out += quads * kSlot) {
-        const FewScale s0 = next[0], s1 = next[1];
-        if (i + 1 < i1) fetch();
-        if (!mbar_try_wait(&full[slot], phase) && !mbar_wait_thread(&full[slot], phase, abort_word, kErrWaitTma)) ok = false;
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
-        // rows g and g + 8: their 16-byte chunks 2 c and 2 c + 1 lie at (chunk ^ g), a phase of 8 lanes (two
-        // rows) reads 8 different bank groups
-        const uint8_t* row = ring + slot * kFewItemBytes + g * 128;
-        const float f0 = few_scale_value(p, s0, mean), f1 = few_scale_value(p, s1, mean);
-        float acc[NT][2][4];
+    tile = 0;
+  }
+  if (p.t) {
+    // t B^T: t as bf16 hi + lo (16 significant bits), one more slot of sums per tile
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // t comes from the grid before
+    constexpr int kSteps = TWO ? 2 : 4;
+    const int first = FLAT ? (int)blockIdx.x * kFewWarps + warp : warp, step = FLAT ? (int)gridDim.x * kFewWarps : kFewWarps;
+    for (int tl = first; tl < nt; tl += step) {
+      const int64_t n0 = (int64_t)(t0 + tl) * kRows + g, n1 = min(n0 + 8, p.N - 1);
+      float acc[NT][4];
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) acc[t][0][k] = acc[t][1][k] = 0.0f;
-        uint4 qa[2], qb[2];
+        for (int k = 0; k < 4; ++k) acc[t][k] = 0.0f;
+      for (int j0 = 4 * c; j0 < p.r + 4 * c; j0 += 16 * kSteps) {
+        // 16 rank columns a step, lane c takes 4 of them; the loads of several steps go out together (one
+        // by one they took 1 us at rank 64)
+        uint2 b0[4], b1[kSteps];
+        float4 tv[NT][kSteps];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          qa[h] = *reinterpret_cast<const uint4*>(row + (((2 * c + h) ^ g) << 4));
-          qb[h] = *reinterpret_cast<const uint4*>(row + 1024 + (((2 * c + h) ^ g) << 4));
-        }
-        const uint32_t wa[8] = {qa[0].x, qa[0].y, qa[0].z, qa[0].w, qa[1].x, qa[1].y, qa[1].z, qa[1].w};
-        const uint32_t wb[8] = {qb[0].x, qb[0].y, qb[0].z, qb[0].w, qb[1].x, qb[1].y, qb[1].z, qb[1].w};
-        const uint64_t v0 = f32_pair(f0, f0), v1 = f32_pair(f1, f1);
-        // the lookups of the next 8 columns are on their way while these are rounded and multiplied
-        uint64_t la[2][4], lb[2][4];
-        few_lookup8(wa[0], lane_addr, la[0]);
-        few_lookup8(wb[0], lane_addr, lb[0]);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (j < 7) {
-            few_lookup8(wa[j + 1], lane_addr, la[(j + 1) & 1]);
-            few_lookup8(wb[j + 1], lane_addr, lb[(j + 1) & 1]);
+        for (int k = 0; k < kSteps; ++k) {
+          const int j = j0 + 16 * k;
+          b0[k] = b1[k] = make_uint2(0u, 0u);
+          if (j < p.r) {
+            b0[k] = __ldg(reinterpret_cast<const uint2*>(p.B + n0 * p.r + j));
+            b1[k] = __ldg(reinterpret_cast<const uint2*>(p.B + n1 * p.r + j));
           }
-          uint32_t a[4], b[4];
-          few_round8(la[j & 1], v0, a);
-          few_round8(lb[j & 1], v1, b);
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
-            const uint4& x = xv[t][j];
-            mma_bf16_16816(acc[t][0], a[0], b[0], a[1], b[1], x.x, x.y);
-            mma_bf16_16816(acc[t][1], a[2], b[2], a[3], b[3], x.z, x.w);
+            tv[t][k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (j < p.r) tv[t][k] = *reinterpret_cast<const float4*>(p.t + (int64_t)min(8 * t + g, p.M - 1) * p.r + j);
           }
         }
-        --pending;
-        __syncwarp();   // every lane has used its codes: the slot takes the item kFewRing ahead
-        const int used = slot;
-        const bool turn = i + 1 == stop && stop < i1;   // to the next quad of columns
-        if (!turn) load_codes(used);
-        if (++slot == kFewRing) {
-          slot = 0;
-          phase ^= 1u;
-        }
-        // sums of rows g and g + 8, tokens 2 c and 2 c + 1 of each group
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          if constexpr (FLAT) {
-            const float both[4] = {acc[t][0][0] + acc[t][1][0], acc[t][0][1] + acc[t][1][1],
-                                   acc[t][0][2] + acc[t][1][2], acc[t][0][3] + acc[t][1][3]};
-            store_flat(quad, tile, t, both);
-          } else {
-            *reinterpret_cast<float2*>(out + t * 128) =
-                make_float2(acc[t][0][0] + acc[t][1][0], acc[t][0][1] + acc[t][1][1]);
-            *reinterpret_cast<float2*>(out + t * 128 + 64) =
-                make_float2(acc[t][0][2] + acc[t][1][2], acc[t][0][3] + acc[t][1][3]);
-          }
-        }
-        if constexpr (FLAT) ++tile;
-        if (turn) {
-          ++quad;
-          load_x(used);
-        }
-      }
-      tile = 0;
-    }
-    if (p.t) {
-      // t B^T: t as bf16 hi + lo (16 significant bits), one more slot of sums per tile
-      asm volatile("griddepcontrol.wait;" ::: "memory");   // t comes from the grid before
-      constexpr int kSteps = TWO ? 2 : 4;
-      const int first = FLAT ? (int)blockIdx.x * kFewWarps + warp : warp, step = FLAT ? (int)gridDim.x * kFewWarps : kFewWarps;
-      for (int tl = first; tl < nt; tl += step) {
-        const int64_t n0 = (int64_t)(t0 + tl) * kRows + g, n1 = min(n0 + 8, p.N - 1);
-        float acc[NT][4];
+        for (int k = 0; k < kSteps; ++k) {
+          if (j0 + 16 * k >= p.r + 4 * c) break;
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) acc[t][k] = 0.0f;
-        for (int j0 = 4 * c; j0 < p.r + 4 * c; j0 += 16 * kSteps) {
-          // 16 rank columns a step, lane c takes 4 of them; the loads of several steps go out together (one
-          // by one they took 1 us at rank 64)
-          uint2 b0[4], b1[kSteps];
-          float4 tv[NT][kSteps];
-#pragma unroll
-          for (int k = 0; k < kSteps; ++k) {
-            const int j = j0 + 16 * k;
-            b0[k] = b1[k] = make_uint2(0u, 0u);
-            if (j < p.r) {
-              b0[k] = __ldg(reinterpret_cast<const uint2*>(p.B + n0 * p.r + j));
-              b1[k] = __ldg(reinterpret_cast<const uint2*>(p.B + n1 * p.r + j));
-            }
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              tv[t][k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-              if (j < p.r) tv[t][k] = *reinterpret_cast<const float4*>(p.t + (int64_t)min(8 * t + g, p.M - 1) * p.r + j);
-            }
-          }
-#pragma unroll
-          for (int k = 0; k < kSteps; ++k) {
-            if (j0 + 16 * k >= p.r + 4 * c) break;
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              uint32_t h0, l0, h1, l1;
-              split_bf16x2(tv[t][k].x, tv[t][k].y, h0, l0);
-              split_bf16x2(tv[t][k].z, tv[t][k].w, h1, l1);
-              mma_bf16_16816(acc[t], b0[k].x, b1[k].x, b0[k].y, b1[k].y, h0, h1);
-              mma_bf16_16816(acc[t], b0[k].x, b1[k].x, b0[k].y, b1[k].y, l0, l1);
-            }
-          }
-        }
-        float* out = sums + (nt * quads + tl) * kSlot + g * 8 + 2 * c;
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          if constexpr (FLAT) {
-            store_flat(quads, tl, t, acc[t]);
-          } else {
-            *reinterpret_cast<float2*>(out + t * 128) = make_float2(acc[t][0], acc[t][1]);
-            *reinterpret_cast<float2*>(out + t * 128 + 64) = make_float2(acc[t][2], acc[t][3]);
+          for (int t = 0; t < NT; ++t) {
+            uint32_t h0, l0, h1, l1;
+            split_bf16x2(tv[t][k].x, tv[t][k].y, h0, l0);
+            split_bf16x2(tv[t][k].z, tv[t][k].w, h1, l1);
+            mma_bf16_16816(acc[t], b0[k].x, b1[k].x, b0[k].y, b1[k].y, h0, h1);
+            mma_bf16_16816(acc[t], b0[k].x, b1[k].x, b0[k].y, b1[k].y, l0, l1);
           }
         }
       }
+      float* out = sums + (nt * quads + tl) * kSlot + g * 8 + 2 * c;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        if constexpr (FLAT) {
+          store_flat(quads, tl, t, acc[t]);
+        } else {
+          *reinterpret_cast<float2*>(out + t * 128) = make_float2(acc[t][0], acc[t][1]);
+          *reinterpret_cast<float2*>(out + t * 128 + 64) = make_float2(acc[t][2], acc[t][3]);
+        }
+      }
     }
-    __syncthreads();
-    if (FLAT || *abort_word) break;   // the same for every thread: all waits of the round are over
-    few_finish<kRows>(p, sums, kSlot, t0, nt, quads, [](int row, int tok) { return (tok >> 3) * 128 + row * 8 + (tok & 7); });
-    __syncthreads();          // the sums are free for the next round
   }
+  __syncthreads();
+  if (!FLAT && !*abort_word)   // the same for every thread: all waits are over
+    few_finish<kRows>(p, sums, kSlot, t0, nt, quads, [](int row, int tok) { return (tok >> 3) * 128 + row * 8 + (tok & 7); });
   if (*abort_word && lane == 0) {
     // a wait ran out: let the copies in flight land before the block's shared memory goes away
     for (int k = 0; k < pending; ++k) {
@@ -636,14 +630,15 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) few_token_ragged_kernel(con
   float* const sums = reinterpret_cast<float*>(few_smem);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
   const int quads = (int)((p.K + kFewCols - 1) / kFewCols);
-  const FewShare share = few_share(sums, (int)(p.N / kRows), quads, kSlot);
+  const FewShare share = few_share((int)(p.N / kRows));
+  const int per_round = few_per_round(share.end - share.begin, quads, kSlot);
   const float mean = p.scale_fp32 ? 0.0f : __ldg(p.mean);
   uint8_t* const stage = few_smem + (kFewRingAddr - smem_u32(few_smem)) + warp * kFewStageBytes;   // hands over x
   few_prefetch_rows(p, (int64_t)share.begin * kRows, (int64_t)share.end * kRows, true);
   const uint32_t lane_addr = few_fill_table(p, few_smem + (kFewTableAddr - smem_u32(few_smem)));
 
-  for (int t0 = share.begin; t0 < share.end; t0 += share.per_round) {
-    const int nt = min(share.end - t0, share.per_round);
+  for (int t0 = share.begin; t0 < share.end; t0 += per_round) {
+    const int nt = min(share.end - t0, per_round);
     const int items = nt * quads;
     const int i0 = items * warp / kFewWarps, i1 = items * (warp + 1) / kFewWarps;
     int quad = i0 / nt, tile = i0 - quad * nt;
@@ -768,19 +763,22 @@ static FewPlan few_token_plan(int64_t M, int64_t K, int64_t N) {
   if (M > kFewTokens || N * K >= (1ll << 37)) return kFewNo;
   const int64_t quads = (K + kFewCols - 1) / kFewCols, tokens = M > 8 ? 16 : 8;
   if (K % 64) return (quads + 1) * tokens * 8 * 4 <= kFewSumBytes ? kFewTiles : kFewNo;
-  const int64_t tiles = (N + 15) / 16, most = (tiles + 147) / 148;   // tiles of the fullest SM
+  const int64_t tiles = (N + 15) / 16, most = (tiles + kFewBlocks - 1) / kFewBlocks;   // tiles of the fullest SM
   const bool fits = most * (quads + 1) * tokens * 16 * 4 <= kFewSumBytes;
-  return fits && most * quads - tiles * quads / 148 <= 12 ? kFewTiles : kFewFlat;
+  return fits && most * quads - tiles * quads / kFewBlocks <= 12 ? kFewTiles : kFewFlat;
 }
 
+// The blocks are those that few_token_plan counts on, one per SM of the whole GPU (a partition of it runs them in turn).
 static cudaError_t launch_few_token_k(void (*kernel)(const FewTokenParams), std::atomic<uint64_t>& configured, int smem,
                                       int64_t blocks, const FewTokenParams& p, cudaStream_t st) {
-  cudaError_t e = enable_smem_once(kernel, smem, configured);
+  int dev = 0, reserved = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&reserved, cudaDevAttrReservedSharedMemoryPerBlock, dev);
+  if (e == cudaSuccess && reserved > kFewReservedBytes) e = cudaErrorInvalidConfiguration;
+  if (e == cudaSuccess) e = enable_smem_once(kernel, smem, configured);
   if (e != cudaSuccess) return e;
-  int dev = 0, sms = 148;
-  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)std::min<int64_t>(sms, blocks));
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>(kFewBlocks, blocks));
   cfg.blockDim = dim3(32 * kFewWarps);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
