@@ -209,9 +209,12 @@ class Act8Tensor:
 
 
 def _require_act8(a: "Act8Tensor", device, what: str) -> None:
+    if not isinstance(a, Act8Tensor) or len(a.shape) != 2:
+        raise QNF4Error(f"{what} must be the 8-bit checkpoint of a matrix")
     M, K = a.shape
     for t, cols, name in ((a.codes, (K + 15) // 16 * 16, "codes"), (a.scales, (K + 31) // 32, "scales")):
-        if t.dtype != torch.uint8 or tuple(t.shape) != (M, cols) or not t.is_contiguous() or t.device != device:
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.uint8 or tuple(t.shape) != (M, cols) \
+                or not t.is_contiguous() or t.device != device:
             raise QNF4Error(f"the {name} of {what} must be a contiguous uint8 tensor [{M}][{cols}] on {device}")
 
 
@@ -364,6 +367,8 @@ def qlora_linear_bwd(dY: torch.Tensor, x, t_saved: torch.Tensor, q: NF4Tensor,
 
 
 def _require(t, dtype, shape, device, name: str) -> None:
+    if not isinstance(t, torch.Tensor):
+        raise QNF4Error(f"{name} must be a tensor, got {type(t).__name__}")
     if t.dtype != dtype or tuple(t.shape) != shape or t.device != device or not t.is_contiguous():
         raise QNF4Error(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {device}, "
                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
@@ -371,8 +376,8 @@ def _require(t, dtype, shape, device, name: str) -> None:
 
 def _require_weight(q: NF4Tensor, device) -> None:
     """The stored parts of a quantized weight: types, sizes and device, as the kernels index them."""
-    if len(q.shape) != 2:
-        raise QNF4Error("the quantized weight must have two dimensions")
+    if not isinstance(q, NF4Tensor) or len(q.shape) != 2:
+        raise QNF4Error("the quantized weight must be an NF4Tensor of two dimensions")
     nb = (q.numel + 63) // 64
     _require_part(q.codes, torch.uint8, 32 * nb, device, "codes")
     if q.double_quant:
@@ -384,8 +389,15 @@ def _require_weight(q: NF4Tensor, device) -> None:
 
 
 def _require_part(t, dtype, count: int, device, name: str) -> None:
-    if t is None or t.dtype != dtype or t.numel() < count or t.device != device or not t.is_contiguous():
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.numel() < count or t.device != device or not t.is_contiguous():
         raise QNF4Error(f"the weight's {name} must hold {count} contiguous {dtype} elements on {device}")
+
+
+def _rank(A) -> int:
+    """Rows of the adapter A, whose other properties _require checks."""
+    if not isinstance(A, torch.Tensor) or A.dim() != 2:
+        raise QNF4Error("A must be a matrix")
+    return A.shape[0]
 
 
 def _empty(rows: int, cols: int, dtype, device) -> torch.Tensor:
@@ -434,12 +446,12 @@ def _addr(t: Optional[torch.Tensor]):
 def _linear_bwd_act8(dY, x: Act8Tensor, t_saved, q: NF4Tensor, A, B, s: float, need_dx: bool, workspace):
     bf16 = torch.bfloat16
     dev = _require_gpu(dY, "dY")
+    _require_act8(x, dev, "x")
     M, K = x.shape
     _require_weight(q, dev)
-    N, r = q.shape[0], A.shape[0]
+    N, r = q.shape[0], _rank(A)
     if q.shape[1] != K:
         raise QNF4Error("shape mismatch between x and W")
-    _require_act8(x, dev, "x")
     _require(dY, bf16, (M, N), dev, "dY")
     _require(t_saved, torch.float32, (M, r), dev, "t_saved")
     _require(A, bf16, (r, K), dev, "A")

@@ -20,7 +20,7 @@ from typing import Optional, Union
 import torch
 
 from .binding import (
-    Act8Tensor, NF4Tensor, QNF4Error, _addr, _empty, _launch, _require, _require_act8, _require_gpu, _require_weight,
+    Act8Tensor, NF4Tensor, QNF4Error, _addr, _empty, _launch, _rank, _require, _require_act8, _require_gpu, _require_weight,
     _workspace, lib,
 )
 
@@ -56,7 +56,7 @@ def act8_quantize(x: torch.Tensor) -> Act8Tensor:
 
 def act8_dequant(a: Act8Tensor) -> torch.Tensor:
     """The values of an 8-bit checkpoint, as bf16 (exact)."""
-    dev = _require_gpu(a.codes, "a.codes")
+    dev = _require_gpu(getattr(a, "codes", None), "a.codes")
     _require_act8(a, dev, "a")
     M, K = a.shape
     out = _empty(M, K, torch.bfloat16, dev)
@@ -126,7 +126,7 @@ def qlora_linear_epilogue_fwd(x: torch.Tensor, q: NF4Tensor, A: Optional[torch.T
         raise QNF4Error("give both adapters or neither")
     r = 0
     if A is not None:
-        r = A.shape[0]
+        r = _rank(A)
         _require(A, bf16, (r, K), dev, "A")
         _require(B, bf16, (N, r), dev, "B")
     if bias is not None:

@@ -100,3 +100,28 @@ def test_binding_refuses_cpu_and_wrong_operands():
                  lambda: q.qlora_linear_epilogue_fwd(x, None, None, None, 1.0)):
         with pytest.raises(q.QNF4Error):
             call()
+
+
+def test_binding_refuses_operands_that_are_missing():
+    """The checks behind the calls, on CPU tensors: what is no tensor, no checkpoint, no quantized weight."""
+    cpu, bf, u8 = torch.device("cpu"), torch.bfloat16, torch.uint8
+    codes, scales = torch.zeros((4, 64), dtype=u8), torch.zeros((4, 2), dtype=u8)
+    binding._require(torch.zeros(8, dtype=bf), bf, (8,), cpu, "w")
+    binding._require_act8(q.Act8Tensor(codes, scales, (4, 64)), cpu, "x")
+    assert binding._rank(torch.zeros((8, 64))) == 8
+    refused = [
+        lambda: binding._require(None, bf, (8,), cpu, "w"), lambda: binding._require([1.0], bf, (1,), cpu, "w"),
+        lambda: binding._require_act8(None, cpu, "x"), lambda: binding._require_act8(codes, cpu, "x"),
+        lambda: binding._require_act8(q.Act8Tensor(None, scales, (4, 64)), cpu, "x"),
+        lambda: binding._require_act8(q.Act8Tensor(codes, None, (4, 64)), cpu, "x"),
+        lambda: binding._require_act8(q.Act8Tensor(codes, scales, (4, 8, 8)), cpu, "x"),
+        lambda: binding._require_weight(None, cpu), lambda: binding._require_weight(codes, cpu),
+        lambda: binding._require_weight(q.NF4Tensor(None, None, None, None, (64, 64)), cpu),
+        lambda: binding._rank(None), lambda: binding._rank(torch.zeros(8)),
+        lambda: q.act8_dequant(None), lambda: q.act8_dequant(codes), lambda: q.act8_quantize(None),
+        lambda: q.epilogue_bwd(None, None, "silu"), lambda: q.rmsnorm_fwd(None, None),
+    ]
+    for i, call in enumerate(refused):
+        with pytest.raises(q.QNF4Error):
+            call()
+            pytest.fail(f"call {i} was not refused")

@@ -144,3 +144,24 @@ def test_few_tokens_of_rows_too_long_for_the_few_token_path(M, N, K, r):
     """K % 64 != 0 and rows whose sums do not fit: 16-token tiles, with their epilogue in the tiles where
     N fills the SMs, behind a K split otherwise."""
     _against_float64(M, N, K, r, "gelu", 212)
+
+
+def test_missing_operands_are_refused():
+    x = torch.zeros((8, 64), dtype=BF, device="cuda")
+    w, f32 = torch.zeros(64, dtype=BF, device="cuda"), torch.zeros(8, device="cuda")
+    W = q.nf4_quantize_dq(_normal((128, 64), 0.02, 1).cuda())
+    A, B = torch.zeros((8, 64), dtype=BF, device="cuda"), torch.zeros((128, 8), dtype=BF, device="cuda")
+    dY, t, a = torch.zeros((8, 128), dtype=BF, device="cuda"), torch.zeros((8, 8), device="cuda"), q.act8_quantize(x)
+    calls = [
+        lambda: q.qlora_linear_bwd(dY, a, None, W, A, B, 1.0), lambda: q.qlora_linear_bwd(dY, a, t, W, None, None, 1.0),
+        lambda: q.qlora_linear_bwd(dY, a, t, W, A, None, 1.0), lambda: q.qlora_linear_bwd(dY, a, t, None, A, B, 1.0),
+        lambda: q.qlora_linear_bwd(dY, a, t, W, A[0], B, 1.0), lambda: q.qlora_linear_bwd(None, a, t, W, A, B, 1.0),
+        lambda: q.qlora_linear_epilogue_fwd(x, None, A, B, 1.0), lambda: q.qlora_linear_epilogue_fwd(x, W, A[0], B, 1.0),
+        lambda: q.qlora_linear_epilogue_fwd(x, W, 3, B, 1.0), lambda: q.qlora_linear_epilogue_fwd(x, W, A, B, 1.0, bias=0.5),
+        lambda: q.rmsnorm_fwd(x, None), lambda: q.rmsnorm_bwd(x, None, f32, w), lambda: q.rmsnorm_bwd(x, x, None, w),
+        lambda: q.rmsnorm_bwd(x, x, f32, None), lambda: q.epilogue_bwd(x, 1.0, "silu"),
+    ]
+    for i, call in enumerate(calls):
+        with pytest.raises(q.QNF4Error):
+            call()
+            pytest.fail(f"call {i} was not refused")
