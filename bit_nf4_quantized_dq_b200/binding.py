@@ -197,7 +197,8 @@ class NF4Tensor:
 
 class Act8Tensor:
     """An 8-bit checkpoint of a bf16 tensor [M][K]: E4M3 codes [M][ld] (ld = K rounded up to 16)
-    and scale bytes [M][ceil(K / 32)], one power of two per row and 32 features."""
+    and scale bytes [M][ceil(K / 32)], one power of two per row and 32 features: E4M3(code) * 2^(byte - 127),
+    NaN for the codes 0x7F and 0xFF and for the byte 255."""
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, shape):
         self.codes = codes
@@ -321,7 +322,10 @@ def nf4_dequant(q: NF4Tensor, out: Optional[torch.Tensor] = None) -> torch.Tenso
 
 def qlora_linear_fwd(x: torch.Tensor, q: NF4Tensor, A: torch.Tensor, B: torch.Tensor, s: float,
                      workspace: Optional[torch.Tensor] = None):
-    """y = x W'^T + s (x A^T) B^T.  Returns (y, t_saved)."""
+    """y = x W'^T + s (x A^T) B^T.  Returns (y, t_saved).
+
+    This call takes every token count through the same tiles.  For up to 16 tokens qlora_linear_epilogue_fwd(x, q,
+    A, B, s, save=True) gives the same y and t, up to the order of their sums, in 0.4 to 0.8 of the time."""
     _require_cuda(x, A, B)
     M, K = x.shape
     N = q.shape[0]
@@ -344,7 +348,8 @@ def qlora_linear_fwd(x: torch.Tensor, q: NF4Tensor, A: torch.Tensor, B: torch.Te
 def qlora_linear_bwd(dY: torch.Tensor, x, t_saved: torch.Tensor, q: NF4Tensor,
                      A: torch.Tensor, B: torch.Tensor, s: float, need_dx: bool = True,
                      workspace: Optional[torch.Tensor] = None):
-    """Returns (dX or None, dA, dB).  x is the forward's bf16 input, or an Act8Tensor of it."""
+    """Returns (dX or None, dA, dB).  x is the forward's bf16 input, or an Act8Tensor of it: dX is then the same, dA
+    and dB those of the decoded values, up to the order in which the sums of the splits of the tokens are joined."""
     if isinstance(x, Act8Tensor):
         return _linear_bwd_act8(dY, x, t_saved, q, A, B, s, need_dx, workspace)
     _require_cuda(dY, x, t_saved, A, B)

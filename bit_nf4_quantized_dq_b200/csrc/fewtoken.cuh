@@ -21,7 +21,7 @@
 //    more than an empty loop, at 36 MB.)  The 128-byte swizzle lets the lanes read them without bank
 //    conflicts.  The scales are one item ahead in registers.
 //  - tcgen05 would need the tile staged for 128 rows and at least 16 tokens; as 16-token tiles of the
-//    fused GEMM (with its K splits and a reduction) the same layer takes 54 us, here 22 us.
+//    fused GEMM (with its K splits and a reduction) the same layer takes 54 us, here 21 us.
 // With K % 64 != 0 code rows are only 4-byte aligned and blocks span rows: a kernel of its own reads
 // the codes into registers, in tiles of 8 rows.
 #pragma once
@@ -224,8 +224,8 @@ __device__ __forceinline__ int few_per_round(int tiles, int quads, int slot) {
 // past K.  Read directly, an instruction asks for 16 bytes of 32 different lines; so the warp reads whole
 // rows of 512 bytes, four tokens at a time, and hands them over through 2 KB of shared memory: 16-byte
 // piece j of lane column c of row i lies at j ^ (c + 4 i), so that neither side meets a bank conflict.
-// 13824 x 5120, 8 tokens: 25.5 us, direct 28.6; 5120 x 13816 (ragged), 8 tokens 38.5 and 45.4, 16 tokens
-// 63.7 and 80.  Tokens past M keep what the buffer held; nothing reads their sums.
+// 13824 x 5120, 8 tokens: 24.6 us, direct 26.6; 5120 x 13816 (ragged), 8 tokens 41.7 and 51.8, 16 tokens
+// 68.8 and 103.  Tokens past M keep what the buffer held; nothing reads their sums.
 template <int NT>
 __device__ __forceinline__ void few_load_x(const FewTokenParams& p, int quad, uint8_t* stage, uint4 (&xv)[NT][8]) {
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
@@ -289,8 +289,8 @@ __device__ __forceinline__ void few_finish(const FewTokenParams& p, const float*
 // FLAT: the blocks share one list of all items, columns outermost, whatever tile they cut; every item
 // leaves its sums in p.part for few_token_join_kernel.
 // Registers: 128 are what 16 warps can have.  With 112, and as much of the SM set aside for shared memory
-// by the down-projection, a block of that fits beside one of this: 24.4 instead of 26.5 us for one token
-// of 5120 x 13824 as a flat list; the tile form does not gain.
+// by the down-projection, a block of that fits beside one of this: 8 % for one token of 5120 x 13824 as a
+// flat list (25.1 us); the tile form does not gain.
 template <bool TWO, bool FLAT>
 __global__ void __maxnreg__(TWO || !FLAT ? 128 : 112) few_token_kernel(const __grid_constant__ FewTokenParams p) {
   constexpr int kRows = 16, NT = TWO ? 2 : 1, kSlot = NT * kRows * 8;   // sums [group of 8 tokens][row][token]
@@ -747,10 +747,10 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) few_token_ragged_kernel(con
 
 // How this path takes a shape.  Whole tiles join their sums in the block that owns them, where all of
 // a block's sums fit and the tiles load the SMs evenly.  Otherwise a flat list of the items over all
-// blocks loads them evenly and a second kernel joins, about 1 us more: with adapters and one token 22.8
-// against 21.8 us for 13824 x 5120 and 11 against 9.7 us for 4096 x 4096, but 24.4 against 31.6 us for
-// 5120 x 13824 (two or three tiles of 54 items per SM), and 43 against 52 us for 16 tokens of 13824 x
-// 5120, whose sums would take two rounds; near the rule's 12 items they are equal (4096 x 11008: 18.0, 18.2).
+// blocks loads them evenly and a second kernel joins, 1 to 3 us more: with adapters and one token 23.8
+// against 20.7 us for 13824 x 5120 and 12.7 against 10.6 us for 4096 x 4096.  The rule's bound, 12 items more on
+// the fullest SM than on average, lies between 4096 x 11008 (12 items; 1 token 17.9 us as tiles, 19.3 as a list, 8
+// tokens 21.7 and 20.8) and 5120 x 5120 (17 items; 1 token 13.9 and 14.9, 16 tokens 25.6 and 24.4).
 // With K % 64 != 0 the other side is 16-token tiles of the fused GEMM with the same epilogue (SiLU, residual, rank
 // 64): 1 token 26.6 against 85 us for 13824 x 5112, 11.2 against 31 for 4000 x 3000, 18 against 43 for 128 x
 // 30008; 16 tokens 45.5 against 85, 16.8 against 31 and 39 against 42.  Rows of thousands of columns in two and more

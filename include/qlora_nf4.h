@@ -333,7 +333,7 @@ int qlora_linear_bwd_act8(const uint16_t* dY, const uint8_t* x_codes, const uint
  * The workspace is needed with dweight only: qlora_rmsnorm_bwd_workspace_bytes(M, K) bytes,
  * 256-byte aligned.
  * Sums are fp32, that of the squares too: a row whose squares sum to more than 3.4e38 gets rstd = 0
- * and y = 0 (NaN where v itself is not finite).  Requirements: K % 8 == 0, eps finite and >= 0, bf16 operands and codes 16-byte
+ * and y = 0 (NaN where v itself is not finite).  With eps = 0 a row of zeros gets rstd = infinity and y = NaN.  Requirements: K % 8 == 0, eps finite and >= 0, bf16 operands and codes 16-byte
  * aligned.  No output may overlap an input or another output.
  * ------------------------------------------------------------------------------------- */
 int qlora_rmsnorm_fwd(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int64_t M, int64_t K,
@@ -355,8 +355,10 @@ int qlora_rmsnorm_bwd(const uint16_t* dy, const uint16_t* dh, const uint16_t* h,
  *   A and B may both be NULL with r = 0: a base without adapters (qlora_merge_requantize).
  *   t_saved : float[M][r] or NULL     z_saved : bf16[M][N] receiving z, or NULL; both are what the
  *     backward pass reads (serving passes NULL)
- * z, the activation and the sum with the residual are fp32; y is rounded once.  Everything else
- * is as for qlora_linear_fwd_ex.  No output may overlap an input or another output.  Workspace:
+ * z, the activation and the sum with the residual are fp32; y is rounded once.  t_saved is rounded
+ * once from a longer sum, as in qlora_linear_fwd_ex, above 16 tokens; up to 16 tokens it is a plain fp32
+ * sum, off by at most (K / 512 + 20) 2^-24 of the sum of its terms' magnitudes.  Everything else is as for
+ * qlora_linear_fwd_ex.  No output may overlap an input or another output.  Workspace:
  * qlora_linear_epi_fwd_workspace_bytes(M, K, N, r) bytes, 256-byte aligned.
  *
  * qlora_epilogue_bwd: dZ = dY * act'(z) (bf16[M][N]) and dbias = sum over tokens of dZ before its

@@ -125,7 +125,8 @@ def _against_float64(M, N, K, r, act, seed):
         tr = 0.5 * (x.double() @ A.double().T)
         zr += tr @ B.double().T
         mag = 0.5 * (x.double().abs() @ A.double().abs().T)
-        assert ((t.double() - tr).abs() <= 128 * 2.0 ** -23 * mag).all()
+        # a thread's share of K / 256 products in two chains, then 13 additions and the factor
+        assert ((t.double() - tr).abs() <= (K / 512 + 20) * U * mag).all()
     zr = zr.cpu().numpy()
     assert_within_tolerance(z, zr, "z")
     assert_within_tolerance(y, ob.act(zr, act) + to_np64(res), "y")
