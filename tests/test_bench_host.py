@@ -134,3 +134,30 @@ def test_timed_region_two_gloo_ranks(tmp_path):
     out = str(tmp_path / "res")
     mp.start_processes(_orchestration_worker, args=(2, port, out), nprocs=2, start_method="spawn", join=True)
     assert open(out + ".0").read() == "ok" and open(out + ".1").read() == "ok"
+
+
+def _includes(name, seen):
+    """`name` and every source of the kernels that it includes, directly or not."""
+    import re
+    csrc = os.path.join(ROOT, "bit_nf4_quantized_dq_b200", "csrc")
+    if name not in seen and os.path.exists(os.path.join(csrc, name)):
+        seen.add(name)
+        for f in re.findall(r'^#include "([^"]+)"', open(os.path.join(csrc, name)).read(), flags=re.M):
+            _includes(f, seen)
+    return seen
+
+
+def test_fused_sources_are_all_that_the_gemm_compiles_in(tmp_path, monkeypatch):
+    want = _includes("gemm.cuh", set())
+    assert {"gemm.cuh", "epilogue.cuh", "codebook.h"} <= want and want <= set(bench.FUSED_SOURCES)
+    # an edit of any of them withdraws the figures, whatever sources they were captured on
+    csrc = tmp_path / "bit_nf4_quantized_dq_b200" / "csrc"
+    shutil.copytree(os.path.join(ROOT, "bit_nf4_quantized_dq_b200", "csrc"), csrc)
+    monkeypatch.setitem(bench.FUSED_TRAFFIC, "sources_sha256", _sources_hash(ROOT))
+    monkeypatch.setattr(bench, "ROOT", str(tmp_path))
+    assert bench.fused_traffic("dx") == bench.FUSED_TRAFFIC["dx"]
+    for f in sorted(want):
+        text = (csrc / f).read_bytes()
+        (csrc / f).write_bytes(text + b"// edited\n")
+        assert bench.fused_traffic("dx") is None, f
+        (csrc / f).write_bytes(text)
