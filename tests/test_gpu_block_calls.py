@@ -166,3 +166,39 @@ def test_missing_operands_are_refused():
         with pytest.raises(q.QNF4Error):
             call()
             pytest.fail(f"call {i} was not refused")
+
+
+@pytest.mark.parametrize("M,N,K,r", [(3, 264, 512, 8), (8, 5120, 4096, 16), (9, 264, 512, 0), (16, 1000, 4096, 8), (5, 136, 1000, 8),
+                                     (16, 136, 1000, 8), (40, 264, 520, 16), (300, 264, 512, 8)])
+def test_tokens_do_not_touch_one_another(M, N, K, r):
+    """NaN and infinities in one token's x and residual leave every other token's outputs as they were, bit for
+    bit, in a workspace full of NaN as well."""
+    inp = synth.linear_inputs(M, N, K, max(r, 8), 221)
+    A, B = (inp["A"].cuda(), inp["B"].cuda()) if r else (None, None)
+    x, res = inp["x"].cuda(), _normal((M, N), 2.0, 222).cuda()
+    W = q.nf4_quantize_dq(_normal((N, K), 0.02, 223).cuda())
+    y, _, z = q.qlora_linear_epilogue_fwd(x, W, A, B, 0.5, activation="silu", residual=res, save=True)
+    for bad in (0, M // 2, M - 1):
+        xb, rb = x.clone(), res.clone()
+        xb[bad, ::3], xb[bad, 1::3], rb[bad] = float("nan"), float("inf"), float("-inf")
+        ws = torch.full((1 << 24,), 0xFF, dtype=torch.uint8, device="cuda")
+        yb, _, zb = q.qlora_linear_epilogue_fwd(xb, W, A, B, 0.5, activation="silu", residual=rb, save=True, workspace=ws)
+        keep = torch.arange(M, device="cuda") != bad
+        assert torch.equal(yb[keep], y[keep]) and torch.equal(zb[keep], z[keep])
+        assert torch.isnan(yb[bad]).all() and torch.isnan(zb[bad]).all()
+    torch.cuda.synchronize()
+    assert q.check_device_error() == 0
+
+
+@pytest.mark.parametrize("M,N,K,r", [(70, 136, 320, 16), (600, 264, 1000, 8), (2100, 128, 256, 64)])
+def test_linear_bwd_act8_in_a_workspace_full_of_nan(M, N, K, r):
+    """With and without splits of the tokens: nothing is read that the call has not written."""
+    inp = synth.linear_inputs(M, N, K, r, 231)
+    x, A, B, dY = (inp[k].cuda() for k in ("x", "A", "B", "dY"))
+    W = q.nf4_quantize_dq(_normal((N, K), 0.02, 232).cuda())
+    _, t = q.qlora_linear_fwd(x, W, A, B, 0.5)
+    a = q.act8_quantize(x)
+    want = q.qlora_linear_bwd(dY, a, t, W, A, B, 0.5)
+    ws = torch.full((1 << 26,), 0xFF, dtype=torch.uint8, device="cuda")
+    got = q.qlora_linear_bwd(dY, a, t, W, A, B, 0.5, workspace=ws)
+    assert all(torch.equal(g, w) for g, w in zip(got, want))
